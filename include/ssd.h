@@ -44,7 +44,9 @@
  * Beyond the scan, on the same conventions: the one-token decode step on the
  * persistent state (ssd_decode_step_bf16 / _i8), the SSD epilogue of the W8A8
  * pipeline (RMSNorm + INT8 output projection with the mean correction,
- * ssd_out_proj_i8) and a self-test of the device-side bounded wait.
+ * ssd_out_proj_i8), the rest of a W8A8 Mamba-2 layer (ssd_add_rmsnorm_i8,
+ * ssd_gated_rmsnorm_i8, ssd_matmul_i8, ssd_conv_fwd_bf16, ssd_conv_step_bf16) and a
+ * self-test of the device-side bounded wait.
  */
 #ifndef SSD_B200_H
 #define SSD_B200_H
@@ -310,6 +312,87 @@ ssd_status ssd_out_proj_i8(int tokens, int d_inner, int d_model, const uint16_t*
                            size_t workspace_bytes, cudaStream_t stream);
 /* Synchronises `stream` and returns the status word of an ssd_out_proj_i8 workspace. */
 ssd_status ssd_out_proj_status(void* workspace, int tokens, int d_inner, cudaStream_t stream);
+
+/* The rest of a W8A8 Mamba-2 layer: what lies between the residual stream and the scan's
+ * inputs, and between the scan's y and the residual stream.  In a layer's order:
+ *   ssd_add_rmsnorm_i8 -> ssd_matmul_i8 (in_proj; its rows are z | x | B | C | dt) ->
+ *   ssd_conv_fwd_bf16 or ssd_conv_step_bf16 -> a scan or a decode step ->
+ *   ssd_gated_rmsnorm_i8 -> ssd_matmul_i8 (out_proj)
+ * Nothing but the numbers below is kept from one call for the next. */
+
+/* Residual addition and RMSNorm of each token, to INT8 codes with one scale per token:
+ *   v = x + residual              (fp32; residual null: v = x), kept as residual_out
+ *   u = v * weight / sqrt(mean(v^2) + eps)           (over the d features)
+ *   scale = max|u| / 127,   q = rint(u / scale)      (|q| <= 127)
+ * A token of zeros (max|v * weight| below 2^-100) gets codes 0 and scale 1; one with a value
+ * that is not finite, or whose sum of squares is not, codes 0 and scale NaN.
+ * x : device bf16 [tokens, d]
+ * residual, residual_out : device [tokens, d], fp32 if residual_fp32 != 0, else bf16 (then v
+ *   is rounded to bf16 before it is normalised).  residual may be null (residual_out is then
+ *   bf16: residual_fp32 must be 0); residual_out may be null, and may be `residual` or `x`
+ *   itself where the types agree, but must not overlap them otherwise.
+ * weight : device fp32 [d] or null (ones), finite.    eps > 0
+ * q : device int8 [tokens, d], written.   scale : device fp32 [tokens], written.
+ * d % 16 == 0 and d <= 32768, else SSD_ERR_UNSUPPORTED. */
+ssd_status ssd_add_rmsnorm_i8(int tokens, int d, const uint16_t* x, const void* residual, int residual_fp32,
+                              const float* weight, float eps, void* residual_out, int8_t* q, float* scale,
+                              cudaStream_t stream);
+
+/* The gated RMSNorm between the scan and the output projection, to the same codes:
+ *   v = y * z / (1 + exp(-z)),   then u, scale and q as in ssd_add_rmsnorm_i8.
+ * y : device bf16 [tokens, d] (the scan's y seen as [B*L, H*P])
+ * z : device bf16, rows of d features ld_z >= d elements apart (a slice of in_proj's rows);
+ *   ld_z % 8 == 0.  Other arguments as in ssd_add_rmsnorm_i8. */
+ssd_status ssd_gated_rmsnorm_i8(int tokens, int d, const uint16_t* y, const uint16_t* z, long long ld_z,
+                                const float* weight, float eps, int8_t* q, float* scale, cudaStream_t stream);
+
+/* INT8 matrix product with a scale per token and per output channel (a projection):
+ *   out[t,n] = s_t[t] * s_w[n] * sum_k q[t,k] * Wq[n,k] + bias[n]       (bf16)
+ * The sum is exact in INT32 (k <= 131072); the scaling is fp32, rounded once to bf16.
+ * q : device int8 [tokens, k]     s_t : device fp32 [tokens]
+ * Wq : device int8 [n, k]         s_w : device fp32 [n]      bias : device fp32 [n] or null
+ * out : device bf16 [tokens, n], written
+ * status : device int, left alone unless a device-side bounded wait expires, which writes
+ *   SSD_ERR_TIMEOUT: clear it once, read it with ssd_workspace_status(status, stream).  Calls
+ *   may share it.
+ * k % 16 == 0 and k <= 131072, else SSD_ERR_UNSUPPORTED; any tokens >= 0 and n >= 1. */
+ssd_status ssd_matmul_i8(int tokens, int k, int n, const int8_t* q, const float* s_t, const int8_t* Wq,
+                         const float* s_w, const float* bias, uint16_t* out, int* status, cudaStream_t stream);
+
+/* The short causal convolution ahead of the scan, with SiLU, and the scan's dt: over the
+ * H*P + 2*G*N channels (x | B | C) of each batch row, with s the row's inputs and its
+ * state's width - 1 inputs in front,
+ *   u[t,c] = bias[c] + sum_{i < width} weight[i,c] * s[t - (width-1) + i, c]
+ *   x | B | C = u / (1 + exp(-u)),        dt = log(1 + exp(dt_raw + dt_bias))
+ * shape : batch, seqlen, nheads, headdim, ngroups, dstate; chunk is not used.  nheads *
+ *   headdim and ngroups * dstate must be multiples of 8 (else SSD_ERR_UNSUPPORTED).
+ * width : 2, 3 or 4 (else SSD_ERR_UNSUPPORTED)
+ * xbc : device bf16, batch * seqlen rows of H*P + 2*G*N channels, ld elements apart
+ * dt_raw : device bf16, as many rows of H, ld elements apart; 2-byte alignment is enough.
+ *   xbc and dt_raw are slices of in_proj's rows, so ld >= H*P + 2*G*N; ld % 8 == 0.
+ *   dt_raw, dt_bias and dt may all be null: no dt is formed.
+ * weight : device fp32 [width, H*P + 2*G*N], bias : device fp32 [H*P + 2*G*N] or null,
+ * dt_bias : device fp32 [H]
+ * lengths : device int [batch] or null: the tokens of each row (clamped to 0..seqlen) in a
+ *   batch padded to seqlen.  Behind a row's last token x, B, C and dt are written as zeros,
+ *   on which the scan leaves the row's state as it is.
+ * initial_state : device bf16 [batch, width-1, H*P + 2*G*N], the inputs ahead of each row,
+ *   oldest first, or null: zeros
+ * x [B,L,H,P], B, C [B,L,G,N] : device bf16, written.   dt : device fp32 [B,L,H], written
+ * final_state : device bf16, the layout of initial_state, written: the last width-1 inputs
+ *   of each row (those of initial_state among them where the row is shorter), or null.  It
+ *   must not overlap initial_state (SSD_ERR_INVALID_ARG). */
+ssd_status ssd_conv_fwd_bf16(const ssd_shape* shape, int width, const uint16_t* xbc, const uint16_t* dt_raw,
+                             long long ld, const float* weight, const float* bias, const float* dt_bias,
+                             const int* lengths, const uint16_t* initial_state, uint16_t* x, float* dt, uint16_t* B,
+                             uint16_t* C, uint16_t* final_state, cudaStream_t stream);
+
+/* One token of ssd_conv_fwd_bf16 on the state, in place (serving; ahead of a decode step):
+ * shape.seqlen must be 1; xbc and dt_raw have batch rows, ld elements apart; state : device
+ * bf16 [batch, width-1, H*P + 2*G*N], read and overwritten; x [B,H,P], dt [B,H], B, C [B,G,N]. */
+ssd_status ssd_conv_step_bf16(const ssd_shape* shape, int width, const uint16_t* xbc, const uint16_t* dt_raw,
+                              long long ld, const float* weight, const float* bias, const float* dt_bias,
+                              uint16_t* state, uint16_t* x, float* dt, uint16_t* B, uint16_t* C, cudaStream_t stream);
 
 /* Self-test of the device-side bounded wait (the mechanism behind SSD_ERR_TIMEOUT):
  * launches, on `stream`, one CTA of two warps that wait on mbarriers nothing ever

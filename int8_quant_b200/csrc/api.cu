@@ -492,6 +492,123 @@ ssd_status ssd_decode_step_i8(const ssd_shape* shape, const uint16_t* x, const f
     return SSD_OK;
 }
 
+// d of a norm's rows: whole 16-byte vectors of codes, and at most 32 features a thread.
+static ssd_status norm_dims(int tokens, int d, float eps) {
+    if (tokens < 0 || d < 1 || !(eps > 0.f)) return SSD_ERR_INVALID_ARG;
+    return d % 16 != 0 || d > 32768 ? SSD_ERR_UNSUPPORTED : SSD_OK;
+}
+
+ssd_status ssd_add_rmsnorm_i8(int tokens, int d, const uint16_t* x, const void* residual, int residual_fp32,
+                              const float* weight, float eps, void* residual_out, int8_t* q, float* scale,
+                              cudaStream_t stream) {
+    const ssd_status st = norm_dims(tokens, d, eps);
+    if (st != SSD_OK) return st;
+    if (!residual && residual_fp32) return SSD_ERR_INVALID_ARG;
+    if (tokens == 0) return SSD_OK;
+    if (!x || !q || !scale) return SSD_ERR_INVALID_ARG;
+    if (!aligned16(x) || !aligned16(residual) || !aligned16(weight) || !aligned16(residual_out) || !aligned16(q) ||
+        !aligned16(scale))
+        return SSD_ERR_INVALID_ARG;
+    SSD_STAGE("add_rmsnorm", launch_add_rmsnorm_i8(tokens, d, x, residual, residual_fp32 != 0, weight, eps,
+                                                   residual_out, q, scale, stream));
+    return SSD_OK;
+}
+
+ssd_status ssd_gated_rmsnorm_i8(int tokens, int d, const uint16_t* y, const uint16_t* z, long long ld_z,
+                                const float* weight, float eps, int8_t* q, float* scale, cudaStream_t stream) {
+    const ssd_status st = norm_dims(tokens, d, eps);
+    if (st != SSD_OK) return st;
+    if (ld_z < d || ld_z % 8 != 0) return SSD_ERR_INVALID_ARG;
+    if (tokens == 0) return SSD_OK;
+    if (!y || !z || !q || !scale) return SSD_ERR_INVALID_ARG;
+    if (!aligned16(y) || !aligned16(z) || !aligned16(weight) || !aligned16(q) || !aligned16(scale))
+        return SSD_ERR_INVALID_ARG;
+    SSD_STAGE("gated_rmsnorm", launch_gated_rmsnorm_i8(tokens, d, y, z, ld_z, weight, eps, q, scale, stream));
+    return SSD_OK;
+}
+
+ssd_status ssd_matmul_i8(int tokens, int k, int n, const int8_t* q, const float* s_t, const int8_t* Wq,
+                         const float* s_w, const float* bias, uint16_t* out, int* status, cudaStream_t stream) {
+    if (tokens < 0 || k < 1 || n < 1) return SSD_ERR_INVALID_ARG;
+    // rows of codes are TMA rows (16-byte strides); |sum| <= k * 127^2 stays in INT32
+    if (k % 16 != 0 || k > 131072) return SSD_ERR_UNSUPPORTED;
+    if (tokens == 0) return SSD_OK;
+    if (!q || !s_t || !Wq || !s_w || !out || !status) return SSD_ERR_INVALID_ARG;
+    if (!aligned16(q) || !aligned16(s_t) || !aligned16(Wq) || !aligned16(s_w) || !aligned16(bias) || !aligned16(out) ||
+        !aligned16(status))
+        return SSD_ERR_INVALID_ARG;
+    SSD_STAGE("matmul_i8", launch_matmul_i8(tokens, k, n, q, s_t, Wq, s_w, bias, out, status, stream));
+    return SSD_OK;
+}
+
+// Sizes of a convolution call.
+static ssd_status conv_dims(const ssd_shape* s, int width, long long ld, ConvDims* d) {
+    if (!s || s->batch < 0 || s->seqlen < 0 || s->nheads < 1 || s->ngroups < 1 || s->headdim < 1 || s->dstate < 1 ||
+        s->nheads % s->ngroups != 0)
+        return SSD_ERR_INVALID_ARG;
+    const long long hp = (long long)s->nheads * s->headdim, gn = (long long)s->ngroups * s->dstate;
+    if (width < 2 || width > 4 || hp % 8 != 0 || gn % 8 != 0 || hp > (1 << 24) || gn > (1 << 24))
+        return SSD_ERR_UNSUPPORTED;
+    if (ld < hp + 2 * gn || ld % 8 != 0) return SSD_ERR_INVALID_ARG;
+    // the grid (a block per 256 threads; the finest split gives one thread an 8-channel
+    // vector of one token, and one dt) has to stay below 2^31 blocks
+    const long long rows = (long long)s->batch * s->seqlen;
+    if (rows > (1LL << 36) / (hp + 2 * gn + 8LL * s->nheads)) return SSD_ERR_UNSUPPORTED;
+    *d = ConvDims{s->batch, s->seqlen, s->nheads, (int)hp, (int)gn, width};
+    return SSD_OK;
+}
+
+static bool conv_args_ok(const ConvIn& in, const ConvOut& out) {
+    if (!in.xbc || !in.weight || !out.x || !out.B || !out.C) return false;
+    const bool dt = out.dt != nullptr;
+    if (dt != (in.dt_raw != nullptr) || dt != (in.dt_bias != nullptr)) return false;
+    return aligned16(in.xbc) && aligned16(in.weight) && aligned16(in.bias) && aligned16(in.dt_bias) &&
+           aligned16(in.lengths) && aligned16(in.init) && aligned16(out.x) && aligned16(out.dt) && aligned16(out.B) &&
+           aligned16(out.C) && aligned16(out.final_state) && ((uintptr_t)in.dt_raw & 1u) == 0;
+}
+
+ssd_status ssd_conv_fwd_bf16(const ssd_shape* shape, int width, const uint16_t* xbc, const uint16_t* dt_raw,
+                             long long ld, const float* weight, const float* bias, const float* dt_bias,
+                             const int* lengths, const uint16_t* initial_state, uint16_t* x, float* dt, uint16_t* B,
+                             uint16_t* C, uint16_t* final_state, cudaStream_t stream) {
+    ConvDims d;
+    const ssd_status st = conv_dims(shape, width, ld, &d);
+    if (st != SSD_OK) return st;
+    if (d.B == 0) return SSD_OK;
+    const size_t state = (size_t)d.B * (d.W - 1) * (d.HP + 2 * d.GN) * sizeof(uint16_t);
+    if (initial_state && final_state) {
+        const uintptr_t a = (uintptr_t)initial_state, f = (uintptr_t)final_state;
+        if (a < f + state && f < a + state) return SSD_ERR_INVALID_ARG;
+    }
+    if (!aligned16(initial_state) || !aligned16(final_state)) return SSD_ERR_INVALID_ARG;
+    if (d.L == 0) {
+        if (!final_state) return SSD_OK;
+        if (initial_state)
+            return from_cuda(cudaMemcpyAsync(final_state, initial_state, state, cudaMemcpyDeviceToDevice, stream));
+        return from_cuda(cudaMemsetAsync(final_state, 0, state, stream));
+    }
+    const ConvIn in{xbc, dt_raw, ld, weight, bias, dt_bias, lengths, initial_state};
+    const ConvOut out{x, dt, B, C, final_state};
+    if (!conv_args_ok(in, out)) return SSD_ERR_INVALID_ARG;
+    SSD_STAGE("conv_fwd", launch_conv_fwd(d, in, out, stream));
+    return SSD_OK;
+}
+
+ssd_status ssd_conv_step_bf16(const ssd_shape* shape, int width, const uint16_t* xbc, const uint16_t* dt_raw,
+                              long long ld, const float* weight, const float* bias, const float* dt_bias,
+                              uint16_t* state, uint16_t* x, float* dt, uint16_t* B, uint16_t* C, cudaStream_t stream) {
+    ConvDims d;
+    if (shape && shape->seqlen != 1) return SSD_ERR_INVALID_ARG;
+    const ssd_status st = conv_dims(shape, width, ld, &d);
+    if (st != SSD_OK) return st;
+    if (d.B == 0) return SSD_OK;
+    const ConvIn in{xbc, dt_raw, ld, weight, bias, dt_bias, nullptr, nullptr};
+    const ConvOut out{x, dt, B, C, nullptr};
+    if (!state || !aligned16(state) || !conv_args_ok(in, out)) return SSD_ERR_INVALID_ARG;
+    SSD_STAGE("conv_step", launch_conv_step(d, in, state, out, stream));
+    return SSD_OK;
+}
+
 static WsLayout calib_layout(const Dims& p, size_t* fin_off, size_t* amax_off) {
     WsLayout w = ws_layout(p, false, true);
     *fin_off = w.total;

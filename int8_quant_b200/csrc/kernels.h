@@ -84,6 +84,42 @@ cudaError_t launch_out_proj_norm(int T, int K, const uint16_t* y, float s_a, int
 cudaError_t launch_out_proj_gemm(int T, int K, int D, const int8_t* aq, float s_a, const int8_t* Wq, const float* s_w,
                                  const float* corr, uint16_t* out, int32_t* acc_dbg, int* status, cudaStream_t st);
 
+// RMSNorm to INT8 codes with one scale per token (rmsnorm_i8.cu): v = x + residual (null: v = x;
+// fp32 or bf16; v kept in res_out unless null), or v = y * silu(z) with rows of z ld_z apart.
+cudaError_t launch_add_rmsnorm_i8(int T, int d, const uint16_t* x, const void* residual, bool fp32, const float* w,
+                                  float eps, void* res_out, int8_t* q, float* scale, cudaStream_t st);
+cudaError_t launch_gated_rmsnorm_i8(int T, int d, const uint16_t* y, const uint16_t* z, long long ld_z,
+                                    const float* w, float eps, int8_t* q, float* scale, cudaStream_t st);
+
+// out [T,N] (bf16) = (q [T,K] Wq [N,K]^T) * s_t[t] * s_w[n] + bias[n] (matmul_i8.cu).
+cudaError_t launch_matmul_i8(int T, int K, int N, const int8_t* q, const float* s_t, const int8_t* Wq,
+                             const float* s_w, const float* bias, uint16_t* out, int* status, cudaStream_t st);
+
+// The short causal convolution ahead of the scan (conv.cu).
+struct ConvDims {
+    int B, L, H, HP, GN, W;     // HP = H*P, GN = G*N; W taps, 2..4
+};
+struct ConvIn {
+    const uint16_t* xbc;        // [B*L rows, ld apart] of HP + 2 GN channels
+    const uint16_t* dt_raw;     // [B*L rows, ld apart] of H, or null: no dt
+    long long ld;
+    const float* weight;        // [W, HP + 2 GN]
+    const float* bias;          // or null
+    const float* dt_bias;       // [H]
+    const int* lengths;         // [B] or null
+    const uint16_t* init;       // [B, W-1, HP + 2 GN] or null
+};
+struct ConvOut {
+    uint16_t* x;
+    float* dt;
+    uint16_t* B;
+    uint16_t* C;
+    uint16_t* final_state;      // [B, W-1, HP + 2 GN] or null
+};
+cudaError_t launch_conv_fwd(const ConvDims& d, const ConvIn& in, const ConvOut& out, cudaStream_t st);
+cudaError_t launch_conv_step(const ConvDims& d, const ConvIn& in, uint16_t* state, const ConvOut& out,
+                             cudaStream_t st);
+
 // init (fp32 [B,H,P,N]) / init8 (INT8 codes [B,H,P,N]): the state before the first chunk, or null for zero.
 cudaError_t launch_state_passing_bf16(const Dims& d, const void* S, bool s_fp32, const float* decay,
                                       const float* init, uint16_t* Hc, float* final_state, float* amax_h,
