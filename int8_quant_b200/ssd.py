@@ -3,7 +3,8 @@
 Each function has the name of the C entry point it calls and takes torch tensors
 that already live on the GPU (torch is used for device memory and streams only);
 every step of the scan runs in the library's CUDA kernels.  A missing library is
-an ImportError, never a fallback.
+an ImportError, never a fallback.  The scan's functions marshal through ctypes; those of
+the layer around it through _binding.so, which also checks their tensors.
 """
 from __future__ import annotations
 
@@ -281,144 +282,51 @@ def ssd_calibrate_i8(shape, prefix, x, dt, A, B, C, s_B, s_C, s_x, s_s, workspac
 
 
 # ---------------------------------------------------------------- the layer around the scan
-# These bindings check their tensors (type, shape, density, device) as well as marshalling
-# them, and launch on the tensors' device whatever the current one is.
+# These go through _binding.so, which checks the tensors (type, shape, density, device) as well as
+# marshalling them, and launches on the tensors' device whatever the current one is.
 
-def _bad(fn, what):
-    raise SsdError(fn, 1, what)
-
-
-def _dense(fn, name, t, dtype, shape, dev):
-    """Data pointer of a contiguous tensor of this type and shape on device `dev`."""
-    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or t.get_device() != dev:
-        _bad(fn, f"{name} has to be a contiguous {dtype} tensor {tuple(shape)} on cuda:{dev}; it is {t.dtype} "
-                 f"{tuple(t.shape)}, strides {t.stride()}, on {t.device}")
-    return t.data_ptr()
+_BINDING = None
 
 
-def _opt(fn, name, t, dtype, shape, dev):
-    return None if t is None else _dense(fn, name, t, dtype, shape, dev)
+def _binding():
+    global _BINDING
+    if _BINDING is None:
+        _lib()
+        import torch  # noqa: F401  (its libraries are the binding's)
+        try:
+            from . import _binding as m
+        except ImportError as e:
+            raise ImportError(f"_binding.so is not built or does not load; run int8_quant_b200/build.py ({e})") from e
+        _BINDING = m
+    return _BINDING
 
 
-def _device_of(fn, t):
-    dev = t.get_device()
-    if dev < 0:
-        _bad(fn, f"the tensors have to be on a CUDA device, not on {t.device}")
-    return dev
-
-
-def _call(fn, f, dev, stream, *args):
-    """f(*args, stream) with `dev` the current device; stream None: that device's current stream."""
-    import torch
-    if stream is None:
-        raw = torch._C._cuda_getCurrentRawStream(dev)
-    else:
-        raw = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
-    if dev == torch.cuda.current_device():
-        st = f(*args, raw)
-    else:
-        with torch.cuda.device(dev):
-            st = f(*args, raw)
-    if st != SSD_OK:
-        raise SsdError(fn, st)
-
-
-def _rows(fn, name, t, lead, width, dtype, dev):
-    """(data pointer, elements between rows) of a tensor lead + (width,) whose rows are evenly spaced: dense,
-    or a slice of the last axis of a dense tensor."""
-    if t.dtype is not dtype or t.shape != (*lead, width) or t.get_device() != dev:
-        _bad(fn, f"{name} has to be a {dtype} tensor {(*lead, width)} on cuda:{dev}; it is {t.dtype} "
-                 f"{tuple(t.shape)} on {t.device}")
-    st = t.stride()
-    ld, span = None, 1
-    for n, s in zip(reversed(lead), reversed(st[:-1])):       # axes of one element have no stride of their own
-        if n > 1:
-            if ld is None:
-                ld = s
-            elif s != ld * span:
-                _bad(fn, f"{name}'s rows are not evenly spaced: strides {st}")
-            span *= n
-        elif n == 0:
-            ld, span = width, 0
-            break
-    if width > 1 and st[-1] != 1:
-        _bad(fn, f"{name}'s last axis is not contiguous: strides {st}")
-    return t.data_ptr(), ld
+def _handle(stream):
+    return stream if stream is None else stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
 def ssd_add_rmsnorm_i8(x, residual, weight, eps: float, residual_out, q, scale, stream=None):
     """x [T, d] bf16; residual [T, d] fp32 or bf16, or None; weight [d] fp32 or None; residual_out: the residual's
     type (bf16 without one) or None; q [T, d] int8 and scale [T] fp32 are written."""
-    import torch
-    fn = "ssd_add_rmsnorm_i8"
-    if x.dim() != 2:
-        _bad(fn, "x has to be [tokens, d]")
-    shape, dev = x.shape, _device_of(fn, x)
-    T, d = shape
-    kept = torch.bfloat16 if residual is None or residual.dtype is not torch.float32 else torch.float32
-    _call(fn, _lib().ssd_add_rmsnorm_i8, dev, stream, T, d, _dense(fn, "x", x, torch.bfloat16, shape, dev),
-          _opt(fn, "residual", residual, kept, shape, dev), int(kept is torch.float32),
-          _opt(fn, "weight", weight, torch.float32, (d,), dev), eps,
-          _opt(fn, "residual_out", residual_out, kept, shape, dev), _dense(fn, "q", q, torch.int8, shape, dev),
-          _dense(fn, "scale", scale, torch.float32, (T,), dev))
+    bad = (_BINDING or _binding()).add_rmsnorm_i8(x, residual, weight, eps, residual_out, q, scale, _handle(stream))
+    if bad:
+        raise SsdError("ssd_add_rmsnorm_i8", *bad)
 
 
 def ssd_gated_rmsnorm_i8(y, z, weight, eps: float, q, scale, stream=None):
     """y [T, d] bf16; z [T, d] bf16, dense or a slice of wider rows; weight [d] fp32 or None; q [T, d] int8 and
     scale [T] fp32 are written."""
-    import torch
-    fn = "ssd_gated_rmsnorm_i8"
-    if y.dim() != 2:
-        _bad(fn, "y has to be [tokens, d]")
-    shape, dev = y.shape, _device_of(fn, y)
-    T, d = shape
-    zp, ld = _rows(fn, "z", z, (T,), d, torch.bfloat16, dev)
-    _call(fn, _lib().ssd_gated_rmsnorm_i8, dev, stream, T, d, _dense(fn, "y", y, torch.bfloat16, shape, dev), zp,
-          d if ld is None else ld, _opt(fn, "weight", weight, torch.float32, (d,), dev), eps,
-          _dense(fn, "q", q, torch.int8, shape, dev), _dense(fn, "scale", scale, torch.float32, (T,), dev))
+    bad = (_BINDING or _binding()).gated_rmsnorm_i8(y, z, weight, eps, q, scale, _handle(stream))
+    if bad:
+        raise SsdError("ssd_gated_rmsnorm_i8", *bad)
 
 
 def ssd_matmul_i8(q, s_t, Wq, s_w, bias, out, status, stream=None):
     """q [T, K] int8, s_t [T] fp32; Wq [N, K] int8, s_w [N] fp32; bias [N] fp32 or None; out [T, N] bf16 is written;
     status: an int32 tensor of one element, zero before its first use (ssd_workspace_status reads it)."""
-    import torch
-    fn = "ssd_matmul_i8"
-    if q.dim() != 2 or Wq.dim() != 2:
-        _bad(fn, "q has to be [tokens, k] and Wq [n, k]")
-    dev = _device_of(fn, q)
-    T, K = q.shape
-    N = Wq.shape[0]
-    _call(fn, _lib().ssd_matmul_i8, dev, stream, T, K, N, _dense(fn, "q", q, torch.int8, (T, K), dev),
-          _dense(fn, "s_t", s_t, torch.float32, (T,), dev), _dense(fn, "Wq", Wq, torch.int8, (N, K), dev),
-          _dense(fn, "s_w", s_w, torch.float32, (N,), dev), _opt(fn, "bias", bias, torch.float32, (N,), dev),
-          _dense(fn, "out", out, torch.bfloat16, (T, N), dev), _dense(fn, "status", status, torch.int32, (1,), dev))
-
-
-def _conv_args(fn, lead, xbc, dt_raw, weight, bias, dt_bias, x, dt, B, C):
-    """What the two convolution calls share: (shape arguments, device, pointers up to dt_bias, output pointers)."""
-    import torch
-    bf, f32 = torch.bfloat16, torch.float32
-    dev = _device_of(fn, x)
-    n = len(lead)
-    if x.dim() != n + 2 or B.dim() != n + 2 or weight.dim() != 2:
-        _bad(fn, "x has to be [..., H, P], B [..., G, N] and weight [width, channels]")
-    H, P = x.shape[n:]
-    G, N = B.shape[n:]
-    ch = H * P + 2 * G * N
-    xp, ld = _rows(fn, "xbc", xbc, lead, ch, bf, dev)
-    rows = 1
-    for m in lead:
-        rows *= m
-    dp = None
-    if dt_raw is not None:
-        dp, ld_dt = _rows(fn, "dt_raw", dt_raw, lead, H, bf, dev)
-        if rows > 1 and ld_dt != ld:
-            _bad(fn, f"the rows of xbc and dt_raw have to be equally far apart, not {ld} and {ld_dt} elements")
-    ins = (xp, dp, ch if ld is None else ld, _dense(fn, "weight", weight, f32, (weight.shape[0], ch), dev),
-           _opt(fn, "bias", bias, f32, (ch,), dev), _opt(fn, "dt_bias", dt_bias, f32, (H,), dev))
-    outs = (_dense(fn, "x", x, bf, (*lead, H, P), dev), _opt(fn, "dt", dt, f32, (*lead, H), dev),
-            _dense(fn, "B", B, bf, (*lead, G, N), dev), _dense(fn, "C", C, bf, (*lead, G, N), dev))
-    return (H, P, G, N, ch), dev, ins, outs
+    bad = (_BINDING or _binding()).matmul_i8(q, s_t, Wq, s_w, bias, out, status, _handle(stream))
+    if bad:
+        raise SsdError("ssd_matmul_i8", *bad)
 
 
 def ssd_conv_fwd_bf16(xbc, dt_raw, weight, bias, dt_bias, lengths, initial_state, x, dt, B, C, final_state,
@@ -427,33 +335,20 @@ def ssd_conv_fwd_bf16(xbc, dt_raw, weight, bias, dt_bias, lengths, initial_state
     [channels] or None, dt_bias [H] fp32; lengths [b] int32 or None; initial_state [b, width-1, channels] bf16 or
     None; x [b, L, H, P], B and C [b, L, G, N] bf16, dt [b, L, H] fp32 and final_state (or None) are written.
     dt_raw, dt_bias and dt may all be None."""
-    import torch
-    fn = "ssd_conv_fwd_bf16"
-    if x.dim() != 4:
-        _bad(fn, "x has to be [batch, seqlen, H, P]")
-    b, L = x.shape[:2]
-    (H, P, G, N, ch), dev, ins, outs = _conv_args(fn, (b, L), xbc, dt_raw, weight, bias, dt_bias, x, dt, B, C)
-    width = weight.shape[0]
-    state = (b, width - 1, ch)
-    _call(fn, _lib().ssd_conv_fwd_bf16, dev, stream, SsdShape.of(b, L, H, P, G, N, 256), width, *ins,
-          _opt(fn, "lengths", lengths, torch.int32, (b,), dev),
-          _opt(fn, "initial_state", initial_state, torch.bfloat16, state, dev), *outs,
-          _opt(fn, "final_state", final_state, torch.bfloat16, state, dev))
+    bad = (_BINDING or _binding()).conv_fwd_bf16(xbc, dt_raw, weight, bias, dt_bias, lengths, initial_state, x, dt, B,
+                                                 C, final_state, _handle(stream))
+    if bad:
+        raise SsdError("ssd_conv_fwd_bf16", *bad)
 
 
 def ssd_conv_step_bf16(xbc, dt_raw, weight, bias, dt_bias, state, x, dt, B, C, stream=None):
     """One token: xbc [b, H*P + 2*G*N] and dt_raw [b, H] bf16, slices of the same rows; state [b, width-1, channels]
     bf16 is updated; x [b, H, P], B and C [b, G, N] bf16 and dt [b, H] fp32 are written.  Parameters as in
     ssd_conv_fwd_bf16."""
-    import torch
-    fn = "ssd_conv_step_bf16"
-    if x.dim() != 3:
-        _bad(fn, "x has to be [batch, H, P]")
-    b = x.shape[0]
-    (H, P, G, N, ch), dev, ins, outs = _conv_args(fn, (b,), xbc, dt_raw, weight, bias, dt_bias, x, dt, B, C)
-    width = weight.shape[0]
-    _call(fn, _lib().ssd_conv_step_bf16, dev, stream, SsdShape.of(b, 1, H, P, G, N, 256), width, *ins,
-          _dense(fn, "state", state, torch.bfloat16, (b, width - 1, ch), dev), *outs)
+    bad = (_BINDING or _binding()).conv_step_bf16(xbc, dt_raw, weight, bias, dt_bias, state, x, dt, B, C,
+                                                  _handle(stream))
+    if bad:
+        raise SsdError("ssd_conv_step_bf16", *bad)
 
 
 def ssd_workspace_status(workspace, stream=None) -> int:

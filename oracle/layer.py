@@ -32,7 +32,7 @@ def norm_codes(v, weight=None, eps: float = 1e-5) -> dict:
 
 def matmul(q, s_t, Wq, s_w, bias=None) -> dict:
     """{"out", "mag"}: the product in float64 and the magnitude |product| + |bias| its roundings go by."""
-    acc = np.asarray(q, np.int64) @ np.asarray(Wq, np.int64).T
+    acc = np.asarray(q, np.float64) @ np.asarray(Wq, np.float64).T     # exact: the sums stay below 2^53
     prod = acc * np.asarray(s_t, np.float64)[:, None] * np.asarray(s_w, np.float64)[None, :]
     b = np.zeros(acc.shape[1]) if bias is None else np.asarray(bias, np.float64)
     return {"out": prod + b[None, :], "mag": np.abs(prod) + np.abs(b)[None, :]}
