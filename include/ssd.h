@@ -333,10 +333,12 @@ ssd_status ssd_out_proj_status(void* workspace, int tokens, int d_inner, cudaStr
  *   itself where the types agree, but must not overlap them otherwise.
  * weight : device fp32 [d] or null (ones), finite.    eps > 0
  * q : device int8 [tokens, d], written.   scale : device fp32 [tokens], written.
+ * values : device bf16 [tokens, d] or null: the values that the codes stand for, q * scale,
+ *   for what reads the activations in 16 bits and for measuring the quantisation error.
  * d % 16 == 0 and d <= 32768, else SSD_ERR_UNSUPPORTED. */
 ssd_status ssd_add_rmsnorm_i8(int tokens, int d, const uint16_t* x, const void* residual, int residual_fp32,
                               const float* weight, float eps, void* residual_out, int8_t* q, float* scale,
-                              cudaStream_t stream);
+                              uint16_t* values, cudaStream_t stream);
 
 /* The gated RMSNorm between the scan and the output projection, to the same codes:
  *   v = y * z / (1 + exp(-z)),   then u, scale and q as in ssd_add_rmsnorm_i8.
@@ -344,7 +346,8 @@ ssd_status ssd_add_rmsnorm_i8(int tokens, int d, const uint16_t* x, const void* 
  * z : device bf16, rows of d features ld_z >= d elements apart (a slice of in_proj's rows);
  *   ld_z % 8 == 0.  Other arguments as in ssd_add_rmsnorm_i8. */
 ssd_status ssd_gated_rmsnorm_i8(int tokens, int d, const uint16_t* y, const uint16_t* z, long long ld_z,
-                                const float* weight, float eps, int8_t* q, float* scale, cudaStream_t stream);
+                                const float* weight, float eps, int8_t* q, float* scale, uint16_t* values,
+                                cudaStream_t stream);
 
 /* INT8 matrix product with a scale per token and per output channel (a projection):
  *   out[t,n] = s_t[t] * s_w[n] * sum_k q[t,k] * Wq[n,k] + bias[n]       (bf16)

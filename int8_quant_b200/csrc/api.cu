@@ -500,30 +500,32 @@ static ssd_status norm_dims(int tokens, int d, float eps) {
 
 ssd_status ssd_add_rmsnorm_i8(int tokens, int d, const uint16_t* x, const void* residual, int residual_fp32,
                               const float* weight, float eps, void* residual_out, int8_t* q, float* scale,
-                              cudaStream_t stream) {
+                              uint16_t* values, cudaStream_t stream) {
     const ssd_status st = norm_dims(tokens, d, eps);
     if (st != SSD_OK) return st;
     if (!residual && residual_fp32) return SSD_ERR_INVALID_ARG;
     if (tokens == 0) return SSD_OK;
     if (!x || !q || !scale) return SSD_ERR_INVALID_ARG;
     if (!aligned16(x) || !aligned16(residual) || !aligned16(weight) || !aligned16(residual_out) || !aligned16(q) ||
-        !aligned16(scale))
+        !aligned16(scale) || !aligned16(values))
         return SSD_ERR_INVALID_ARG;
     SSD_STAGE("add_rmsnorm", launch_add_rmsnorm_i8(tokens, d, x, residual, residual_fp32 != 0, weight, eps,
-                                                   residual_out, q, scale, stream));
+                                                   residual_out, q, scale, values, stream));
     return SSD_OK;
 }
 
 ssd_status ssd_gated_rmsnorm_i8(int tokens, int d, const uint16_t* y, const uint16_t* z, long long ld_z,
-                                const float* weight, float eps, int8_t* q, float* scale, cudaStream_t stream) {
+                                const float* weight, float eps, int8_t* q, float* scale, uint16_t* values,
+                                cudaStream_t stream) {
     const ssd_status st = norm_dims(tokens, d, eps);
     if (st != SSD_OK) return st;
     if (ld_z < d || ld_z % 8 != 0) return SSD_ERR_INVALID_ARG;
     if (tokens == 0) return SSD_OK;
     if (!y || !z || !q || !scale) return SSD_ERR_INVALID_ARG;
-    if (!aligned16(y) || !aligned16(z) || !aligned16(weight) || !aligned16(q) || !aligned16(scale))
+    if (!aligned16(y) || !aligned16(z) || !aligned16(weight) || !aligned16(q) || !aligned16(scale) ||
+        !aligned16(values))
         return SSD_ERR_INVALID_ARG;
-    SSD_STAGE("gated_rmsnorm", launch_gated_rmsnorm_i8(tokens, d, y, z, ld_z, weight, eps, q, scale, stream));
+    SSD_STAGE("gated_rmsnorm", launch_gated_rmsnorm_i8(tokens, d, y, z, ld_z, weight, eps, q, scale, values, stream));
     return SSD_OK;
 }
 
@@ -550,10 +552,10 @@ static ssd_status conv_dims(const ssd_shape* s, int width, long long ld, ConvDim
     if (width < 2 || width > 4 || hp % 8 != 0 || gn % 8 != 0 || hp > (1 << 24) || gn > (1 << 24))
         return SSD_ERR_UNSUPPORTED;
     if (ld < hp + 2 * gn || ld % 8 != 0) return SSD_ERR_INVALID_ARG;
-    // the grid (a block per 256 threads; the finest split gives one thread an 8-channel
-    // vector of one token, and one dt) has to stay below 2^31 blocks
+    // the grid (at most a block per token and 256 channels, and fewer for dt and the final
+    // state) has to stay below 2^31 blocks
     const long long rows = (long long)s->batch * s->seqlen;
-    if (rows > (1LL << 36) / (hp + 2 * gn + 8LL * s->nheads)) return SSD_ERR_UNSUPPORTED;
+    if (rows > (1LL << 35) / (hp + 2 * gn + 8LL * s->nheads)) return SSD_ERR_UNSUPPORTED;
     *d = ConvDims{s->batch, s->seqlen, s->nheads, (int)hp, (int)gn, width};
     return SSD_OK;
 }

@@ -141,9 +141,9 @@ double as_double(PyObject* o, const char* name) {
     return v;
 }
 
-// (x, residual, weight, eps, residual_out, q, scale, stream)
+// (x, residual, weight, eps, residual_out, q, scale, values, stream)
 PyObject* add_rmsnorm_i8(PyObject*, PyObject* const* a, Py_ssize_t n) {
-    return guarded(n, 8, [&] {
+    return guarded(n, 9, [&] {
         Call c;
         const at::Tensor& x = c.first(a[0], "x");
         if (x.dim() != 2) throw Refused("x has to be [tokens, d], not " + text(x.sizes()));
@@ -159,15 +159,16 @@ PyObject* add_rmsnorm_i8(PyObject*, PyObject* const* a, Py_ssize_t n) {
         void* ro = c.optional<void>(a[4], "residual_out", kept, shape);
         int8_t* q = c.dense<int8_t>(a[5], "q", at::kChar, shape);
         float* s = c.dense<float>(a[6], "scale", at::kFloat, {shape[0]});
-        return c.launch(a[7], [&](cudaStream_t st) {
-            return ssd_add_rmsnorm_i8(T, d, xp, rp, fp32, w, eps, ro, q, s, st);
+        uint16_t* val = c.optional<uint16_t>(a[7], "values", at::kBFloat16, shape);
+        return c.launch(a[8], [&](cudaStream_t st) {
+            return ssd_add_rmsnorm_i8(T, d, xp, rp, fp32, w, eps, ro, q, s, val, st);
         });
     });
 }
 
-// (y, z, weight, eps, q, scale, stream)
+// (y, z, weight, eps, q, scale, values, stream)
 PyObject* gated_rmsnorm_i8(PyObject*, PyObject* const* a, Py_ssize_t n) {
-    return guarded(n, 7, [&] {
+    return guarded(n, 8, [&] {
         Call c;
         const at::Tensor& y = c.first(a[0], "y");
         if (y.dim() != 2) throw Refused("y has to be [tokens, d], not " + text(y.sizes()));
@@ -180,8 +181,9 @@ PyObject* gated_rmsnorm_i8(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const float eps = (float)as_double(a[3], "eps");
         int8_t* q = c.dense<int8_t>(a[4], "q", at::kChar, shape);
         float* s = c.dense<float>(a[5], "scale", at::kFloat, {shape[0]});
-        return c.launch(a[6], [&](cudaStream_t st) {
-            return ssd_gated_rmsnorm_i8(T, d, yp, zp, ld ? ld : d, w, eps, q, s, st);
+        uint16_t* val = c.optional<uint16_t>(a[6], "values", at::kBFloat16, shape);
+        return c.launch(a[7], [&](cudaStream_t st) {
+            return ssd_gated_rmsnorm_i8(T, d, yp, zp, ld ? ld : d, w, eps, q, s, val, st);
         });
     });
 }

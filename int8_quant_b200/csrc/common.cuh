@@ -27,6 +27,88 @@ __device__ __forceinline__ uint16_t float_to_bf16_bits(float f) {
     return __bfloat16_as_ushort(__float2bfloat16_rn(f));
 }
 
+// The 8 bf16 values of a 16-byte vector as fp32, and two fp32 values as packed bf16.
+__device__ __forceinline__ void unpack8(const uint4& v, float (&f)[8]) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        f[2 * e] = __uint_as_float(w[e] << 16);
+        f[2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
+    }
+}
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+__device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
+    return make_uint4(pack2(f[0], f[1]), pack2(f[2], f[3]), pack2(f[4], f[5]), pack2(f[6], f[7]));
+}
+
+// Two fp32 values in a 64-bit register pair, for the packed fp32 instructions of sm_100 (each
+// half rounded as the plain instruction rounds it).
+typedef unsigned long long f32x2;
+__device__ __forceinline__ f32x2 pair2(float lo, float hi) {
+    f32x2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ f32x2 both2(float v) { return pair2(v, v); }
+__device__ __forceinline__ float2 split2(f32x2 a) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a));
+    return r;
+}
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+    f32x2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
+    f32x2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
+    f32x2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint32_t pack2(f32x2 a) {
+    const float2 v = split2(a);
+    return pack2(v.x, v.y);
+}
+// The 8 bf16 values of a 16-byte vector as four pairs, and four pairs as such a vector.
+__device__ __forceinline__ void unpack8(const uint4& v, f32x2 (&f)[4]) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) f[e] = pair2(__uint_as_float(w[e] << 16), __uint_as_float(w[e] & 0xffff0000u));
+}
+__device__ __forceinline__ uint4 pack8(const f32x2 (&f)[4]) {
+    return make_uint4(pack2(f[0]), pack2(f[1]), pack2(f[2]), pack2(f[3]));
+}
+// 8 consecutive fp32 values (16-byte aligned) as four pairs.
+__device__ __forceinline__ void load8(const float* p, f32x2 (&f)[4]) {
+    const float4 a = __ldg(reinterpret_cast<const float4*>(p)), b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+    f[0] = pair2(a.x, a.y);
+    f[1] = pair2(a.z, a.w);
+    f[2] = pair2(b.x, b.y);
+    f[3] = pair2(b.z, b.w);
+}
+
+// silu(u) = u / (1 + exp(-u)) from the fast exponential and reciprocal, a relative error of
+// a few 2^-23 times 1 + |u|: u below -88 gives -0, NaN stays NaN.
+__device__ __forceinline__ f32x2 fast_silu2(f32x2 u) {
+    const float2 t = split2(mul2(u, both2(-1.4426950408889634f)));
+    float2 e, r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.x) : "f"(t.x));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.y) : "f"(t.y));
+    const float2 d = split2(add2(pair2(e.x, e.y), both2(1.0f)));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.x) : "f"(d.x));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.y) : "f"(d.y));
+    return mul2(u, pair2(r.x, r.y));
+}
+
 // ---------------------------------------------------------------- specified fp32 exp
 // exp(x) with a fixed sequence of individually rounded fp32 operations, so that the
 // W8A8 path's integer codes (X_scaled quantisation, decay codes) are reproducible

@@ -86,10 +86,13 @@ cudaError_t launch_out_proj_gemm(int T, int K, int D, const int8_t* aq, float s_
 
 // RMSNorm to INT8 codes with one scale per token (rmsnorm_i8.cu): v = x + residual (null: v = x;
 // fp32 or bf16; v kept in res_out unless null), or v = y * silu(z) with rows of z ld_z apart.
+// values: q * scale as bf16, or null.
 cudaError_t launch_add_rmsnorm_i8(int T, int d, const uint16_t* x, const void* residual, bool fp32, const float* w,
-                                  float eps, void* res_out, int8_t* q, float* scale, cudaStream_t st);
+                                  float eps, void* res_out, int8_t* q, float* scale, uint16_t* values,
+                                  cudaStream_t st);
 cudaError_t launch_gated_rmsnorm_i8(int T, int d, const uint16_t* y, const uint16_t* z, long long ld_z,
-                                    const float* w, float eps, int8_t* q, float* scale, cudaStream_t st);
+                                    const float* w, float eps, int8_t* q, float* scale, uint16_t* values,
+                                    cudaStream_t st);
 
 // out [T,N] (bf16) = (q [T,K] Wq [N,K]^T) * s_t[t] * s_w[n] + bias[n] (matmul_i8.cu).
 cudaError_t launch_matmul_i8(int T, int K, int N, const int8_t* q, const float* s_t, const int8_t* Wq,

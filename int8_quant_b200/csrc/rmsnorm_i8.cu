@@ -9,8 +9,15 @@
 // and the row is read once, kept in registers, and needs one reduction (of v^2 and |p|
 // together) before its codes are written.
 //
-// One CTA per token; each thread holds VPT vectors of 8 features.  Bound by HBM: 11 bytes a
-// feature with an fp32 residual (2 + 4 read, 4 + 1 written), 5 with the gate.
+// Bound by HBM: 11 bytes a feature with an fp32 residual (2 + 4 read, 4 + 1 written), 5 with
+// the gate, 2 more where the codes' values are asked for.  One CTA per token and VPT vectors
+// of 8 features a thread, all loads issued before anything else; many small CTAs resident on
+// an SM cover each other's barrier.  Measured, in a graph (6.53 TB/s is the copy bandwidth):
+//   65536 x 2560, fp32 residual   268 us = 6.9 TB/s       16384 x 5120, gate   80 us = 5.2 TB/s
+// The gate spends two special-function instructions a feature (exponential, reciprocal); with
+// packed fp32 arithmetic it takes half the instructions of the plain form (95 us).  A
+// persistent grid that loads the next token ahead needs twice the registers and was slower:
+// 291 and 94 us.
 #include "kernels.h"
 
 namespace ssd {
@@ -19,6 +26,9 @@ namespace {
 
 enum : int { kResNone = 0, kResF32 = 1, kResBf16 = 2, kGate = 3 };
 
+constexpr int kMaxThreads = 512;
+constexpr float kMagic = 12582912.0f;       // 1.5 * 2^23: adding it rounds a small number to a whole one
+
 struct NormArgs {
     int d;
     long long ld2;              // row stride of the second input (z; d for a residual)
@@ -26,149 +36,178 @@ struct NormArgs {
     const void* in2;            // residual or z (null: none)
     const float* w;             // null: ones
     float eps;
-    void* res_out;              // may be null, may be in2 itself
+    void* res_out;              // may be null, may be in2 or x itself
     int8_t* q;
     float* scale;
+    uint16_t* values;           // q * scale as bf16, or null
 };
 
-__device__ __forceinline__ void unpack8(const uint4& v, float (&f)[8]) {
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        f[2 * e] = __uint_as_float(w[e] << 16);
-        f[2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
-    }
-}
-__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
-    return (uint32_t)float_to_bf16_bits(lo) | ((uint32_t)float_to_bf16_bits(hi) << 16);
-}
-// max that keeps a NaN (fmaxf drops it), so that a row with one is seen
-__device__ __forceinline__ float max_nan(float a, float b) {
-    float r;
-    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
-    return r;
-}
+template <int KIND, int VPT>
+struct RowIn {
+    uint4 x[VPT];
+    uint4 r[VPT][KIND == kResF32 ? 2 : 1];
+};
 
 template <int KIND, int VPT>
-__global__ void __launch_bounds__(1024)
-rmsnorm_i8_kernel(const __grid_constant__ NormArgs a) {
-    const long long row = blockIdx.x;
-    const int nv = a.d >> 3;
-    float p[VPT][8];
-    float ss = 0.f, top = 0.f;
+__device__ __forceinline__ void load_row(const NormArgs& a, long long row, int nv, RowIn<KIND, VPT>& in) {
 #pragma unroll
     for (int k = 0; k < VPT; ++k) {
         const int i = threadIdx.x + k * blockDim.x;
-        if (i >= nv) break;
-        float v[8];
-        unpack8(*(reinterpret_cast<const uint4*>(a.x + row * a.d) + i), v);
-        if (KIND == kGate) {
-            float z[8];
-            unpack8(*(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.in2) + row * a.ld2) + i), z);
+        if (i >= nv) continue;
+        in.x[k] = reinterpret_cast<const uint4*>(a.x + row * a.d)[i];
+        if (KIND == kResF32) {
+            const uint4* rp = reinterpret_cast<const uint4*>(static_cast<const float*>(a.in2) + row * a.d) + 2 * i;
+            in.r[k][0] = rp[0];
+            in.r[k][KIND == kResF32 ? 1 : 0] = rp[1];
+        } else if (KIND != kResNone) {
+            in.r[k][0] = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.in2) + row * a.ld2)[i];
+        }
+    }
+}
+
+__device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] *= __fdividef(z[e], 1.0f + __expf(-z[e]));
+    for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+    return v;
+}
+__device__ __forceinline__ float warp_max(float v) {
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, off));
+    return v;
+}
+
+// 64 registers up to four vectors a thread: 1024 threads an SM
+template <int KIND, int VPT>
+__global__ void __launch_bounds__(kMaxThreads, VPT == 8 ? 1 : 2)
+rmsnorm_i8_kernel(const __grid_constant__ NormArgs a) {
+    __shared__ float2 part[kMaxThreads / 32];
+    const int nv = a.d >> 3, warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nw = blockDim.x >> 5;
+    const float inf = __int_as_float(0x7f800000);
+    const long long row = blockIdx.x;
+    RowIn<KIND, VPT> in;
+    load_row<KIND, VPT>(a, row, nv, in);
+    f32x2 p[VPT][4];
+    f32x2 ss2 = both2(0.f);
+    float top = 0.f;
+#pragma unroll
+    for (int k = 0; k < VPT; ++k) {
+        const int i = threadIdx.x + k * blockDim.x;
+        if (i >= nv) continue;
+        f32x2 v[4];
+        unpack8(in.x[k], v);
+        if (KIND == kGate) {
+            f32x2 z[4];
+            unpack8(in.r[k][0], z);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e] = mul2(v[e], fast_silu2(z[e]));
         } else if (KIND == kResF32) {
-            const float4* rp = reinterpret_cast<const float4*>(static_cast<const float*>(a.in2) + row * a.d) + 2 * i;
-            const float4 r0 = rp[0], r1 = rp[1];
-            v[0] += r0.x; v[1] += r0.y; v[2] += r0.z; v[3] += r0.w;
-            v[4] += r1.x; v[5] += r1.y; v[6] += r1.z; v[7] += r1.w;
+            const uint4 r0 = in.r[k][0], r1 = in.r[k][KIND == kResF32 ? 1 : 0];
+            const uint32_t r[8] = {r0.x, r0.y, r0.z, r0.w, r1.x, r1.y, r1.z, r1.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                v[e] = add2(v[e], pair2(__uint_as_float(r[2 * e]), __uint_as_float(r[2 * e + 1])));
         } else if (KIND == kResBf16) {
-            float r[8];
-            unpack8(*(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.in2) + row * a.d) + i), r);
+            f32x2 r[4];
+            unpack8(in.r[k][0], r);
             // the norm is of the residual as it is stored: rounded to bf16
 #pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] = bf16_bits_to_float(float_to_bf16_bits(v[e] + r[e]));
+            for (int e = 0; e < 4; ++e) v[e] = add2(v[e], r[e]);
+            unpack8(pack8(v), v);
         }
         if (KIND != kGate && a.res_out) {
             if (KIND == kResF32) {
-                float4* op = reinterpret_cast<float4*>(static_cast<float*>(a.res_out) + row * a.d) + 2 * i;
-                op[0] = make_float4(v[0], v[1], v[2], v[3]);
-                op[1] = make_float4(v[4], v[5], v[6], v[7]);
+                ulonglong2* op = reinterpret_cast<ulonglong2*>(static_cast<float*>(a.res_out) + row * a.d) + 2 * i;
+                op[0] = make_ulonglong2(v[0], v[1]);
+                op[1] = make_ulonglong2(v[2], v[3]);
             } else {
-                reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.res_out) + row * a.d)[i] =
-                    make_uint4(pack2(v[0], v[1]), pack2(v[2], v[3]), pack2(v[4], v[5]), pack2(v[6], v[7]));
+                reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.res_out) + row * a.d)[i] = pack8(v);
             }
         }
-        float w[8] = {1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f};
-        if (a.w) {
-            const float4* wp = reinterpret_cast<const float4*>(a.w) + 2 * i;
-            const float4 w0 = __ldg(wp), w1 = __ldg(wp + 1);
-            w[0] = w0.x; w[1] = w0.y; w[2] = w0.z; w[3] = w0.w;
-            w[4] = w1.x; w[5] = w1.y; w[6] = w1.z; w[7] = w1.w;
-        }
+        f32x2 w[4] = {both2(1.f), both2(1.f), both2(1.f), both2(1.f)};
+        if (a.w) load8(a.w + 8 * i, w);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            ss = fmaf(v[e], v[e], ss);
-            p[k][e] = v[e] * w[e];
-            top = max_nan(top, fabsf(p[k][e]));
+        for (int e = 0; e < 4; ++e) {
+            ss2 = fma2(v[e], v[e], ss2);
+            p[k][e] = mul2(v[e], w[e]);
+            const float2 m = split2(p[k][e]);
+            top = fmaxf(fmaxf(top, fabsf(m.x)), fabsf(m.y));     // a NaN is dropped here, but not by ss2
         }
     }
-    __shared__ float part_s[32], part_m[32];
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) {
-        ss += __shfl_xor_sync(0xffffffffu, ss, off);
-        top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, off));
-    }
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    if (lane == 0) {
-        part_s[warp] = ss;
-        part_m[warp] = top;
-    }
+    float ss = split2(ss2).x + split2(ss2).y;
+    ss = warp_sum(ss);
+    top = warp_max(top);
+    if (lane == 0) part[warp] = make_float2(ss, top);
     __syncthreads();
-    const int nw = blockDim.x >> 5;
-    ss = lane < nw ? part_s[lane] : 0.f;
-    top = lane < nw ? part_m[lane] : 0.f;
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) {
-        ss += __shfl_xor_sync(0xffffffffu, ss, off);
-        top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, off));
-    }
+    const float2 mine = lane < nw ? part[lane] : make_float2(0.f, 0.f);
+    ss = warp_sum(mine.x);
+    top = warp_max(mine.y);
     // A row that is not finite gets the scale NaN and codes 0; a row of zeros (below 2^-100,
     // where 127 / top would overflow) the scale 1 and codes 0.
-    const bool finite = ss < __int_as_float(0x7f800000) && top < __int_as_float(0x7f800000);
+    const bool finite = ss < inf && top < inf;
     const bool some = finite && top >= 0x1p-100f;
     const float inv = some ? 127.0f / top : 0.f;
-    if (threadIdx.x == 0) {
-        const float r = rsqrtf(ss / (float)a.d + a.eps);
-        a.scale[row] = some ? top * r / 127.0f : finite ? 1.0f : __int_as_float(0x7fffffff);
-    }
+    const float scale = some ? top * rsqrtf(ss / (float)a.d + a.eps) / 127.0f
+                             : finite ? 1.0f : __int_as_float(0x7fffffff);
+    if (threadIdx.x == 0) a.scale[row] = scale;
 #pragma unroll
     for (int k = 0; k < VPT; ++k) {
         const int i = threadIdx.x + k * blockDim.x;
-        if (i >= nv) break;
-        uint32_t o[2] = {0u, 0u};
+        if (i >= nv) continue;
+        uint2 o = make_uint2(0u, 0u);
+        f32x2 c[4];
         if (some) {
+            // 1.5 * 2^23 + c has the code's two's complement in its low byte, rounded to nearest
+            // even; |p * inv| <= 127 (1 + 2^-22), so no code passes 127
 #pragma unroll
-            for (int e = 0; e < 8; ++e) o[e >> 2] |= ((uint32_t)quant_i8(p[k][e], inv) & 0xffu) << (8 * (e & 3));
+            for (int e = 0; e < 4; ++e) c[e] = fma2(p[k][e], both2(inv), both2(kMagic));
+            uint32_t h[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                h[e] = __byte_perm(__float_as_uint(split2(c[e]).x), __float_as_uint(split2(c[e]).y), 0x0040);
+            o = make_uint2(__byte_perm(h[0], h[1], 0x5410), __byte_perm(h[2], h[3], 0x5410));
         }
-        reinterpret_cast<uint2*>(a.q + row * a.d)[i] = make_uint2(o[0], o[1]);
+        reinterpret_cast<uint2*>(a.q + row * a.d)[i] = o;
+        if (a.values) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                c[e] = mul2(some ? add2(c[e], both2(-kMagic)) : both2(0.f), both2(scale));
+            reinterpret_cast<uint4*>(a.values + row * a.d)[i] = pack8(c);
+        }
     }
 }
 
-template <int KIND>
-cudaError_t launch_kind(int T, const NormArgs& a, cudaStream_t st) {
+template <int KIND, int VPT>
+cudaError_t launch_vpt(const NormArgs& a, int T, cudaStream_t st) {
     const int nv = a.d >> 3;
-    const int vpt = nv <= 1024 ? 1 : nv <= 2048 ? 2 : 4;
-    const int per = (nv + vpt - 1) / vpt;
-    const int threads = (per + 31) / 32 * 32;
-    if (vpt == 1) rmsnorm_i8_kernel<KIND, 1><<<T, threads, 0, st>>>(a);
-    else if (vpt == 2) rmsnorm_i8_kernel<KIND, 2><<<T, threads, 0, st>>>(a);
-    else rmsnorm_i8_kernel<KIND, 4><<<T, threads, 0, st>>>(a);
+    const int threads = ((nv + VPT - 1) / VPT + 31) / 32 * 32;
+    rmsnorm_i8_kernel<KIND, VPT><<<T, threads, 0, st>>>(a);
     return cudaGetLastError();
+}
+
+// Two vectors a thread up to 320 threads: beyond, CTAs get so large that few fit an SM, and
+// four a thread are faster (16384 tokens with the gate: d = 4096 64 us either way, 5120 80
+// against 81, 8192 168 against 127).
+template <int KIND>
+cudaError_t launch_kind(const NormArgs& a, int T, cudaStream_t st) {
+    if (a.d <= 5120) return launch_vpt<KIND, 2>(a, T, st);
+    if (a.d <= 32 * kMaxThreads) return launch_vpt<KIND, 4>(a, T, st);
+    return launch_vpt<KIND, 8>(a, T, st);
 }
 
 }  // namespace
 
 cudaError_t launch_add_rmsnorm_i8(int T, int d, const uint16_t* x, const void* residual, bool fp32, const float* w,
-                                  float eps, void* res_out, int8_t* q, float* scale, cudaStream_t st) {
-    const NormArgs a{d, d, x, residual, w, eps, res_out, q, scale};
-    if (!residual) return launch_kind<kResNone>(T, a, st);
-    return fp32 ? launch_kind<kResF32>(T, a, st) : launch_kind<kResBf16>(T, a, st);
+                                  float eps, void* res_out, int8_t* q, float* scale, uint16_t* values,
+                                  cudaStream_t st) {
+    const NormArgs a{d, d, x, residual, w, eps, res_out, q, scale, values};
+    if (!residual) return launch_kind<kResNone>(a, T, st);
+    return fp32 ? launch_kind<kResF32>(a, T, st) : launch_kind<kResBf16>(a, T, st);
 }
 
 cudaError_t launch_gated_rmsnorm_i8(int T, int d, const uint16_t* y, const uint16_t* z, long long ld_z,
-                                    const float* w, float eps, int8_t* q, float* scale, cudaStream_t st) {
-    return launch_kind<kGate>(T, NormArgs{d, ld_z, y, z, w, eps, nullptr, q, scale}, st);
+                                    const float* w, float eps, int8_t* q, float* scale, uint16_t* values,
+                                    cudaStream_t st) {
+    return launch_kind<kGate>(NormArgs{d, ld_z, y, z, w, eps, nullptr, q, scale, values}, T, st);
 }
 
 }  // namespace ssd

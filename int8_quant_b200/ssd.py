@@ -125,9 +125,9 @@ def _lib():
         lib.ssd_selftest_bounded_wait.argtypes = [ctypes.c_longlong, P, P, P]
         L, F = ctypes.c_longlong, ctypes.c_float
         lib.ssd_add_rmsnorm_i8.restype = I
-        lib.ssd_add_rmsnorm_i8.argtypes = [I, I, P, P, I, P, F, P, P, P, P]
+        lib.ssd_add_rmsnorm_i8.argtypes = [I, I, P, P, I, P, F, P, P, P, P, P]
         lib.ssd_gated_rmsnorm_i8.restype = I
-        lib.ssd_gated_rmsnorm_i8.argtypes = [I, I, P, P, L, P, F, P, P, P]
+        lib.ssd_gated_rmsnorm_i8.argtypes = [I, I, P, P, L, P, F, P, P, P, P]
         lib.ssd_matmul_i8.restype = I
         lib.ssd_matmul_i8.argtypes = [I, I, I, P, P, P, P, P, P, P, P]
         lib.ssd_conv_fwd_bf16.restype = I
@@ -305,18 +305,20 @@ def _handle(stream):
     return stream if stream is None else stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
-def ssd_add_rmsnorm_i8(x, residual, weight, eps: float, residual_out, q, scale, stream=None):
+def ssd_add_rmsnorm_i8(x, residual, weight, eps: float, residual_out, q, scale, values=None, stream=None):
     """x [T, d] bf16; residual [T, d] fp32 or bf16, or None; weight [d] fp32 or None; residual_out: the residual's
-    type (bf16 without one) or None; q [T, d] int8 and scale [T] fp32 are written."""
-    bad = (_BINDING or _binding()).add_rmsnorm_i8(x, residual, weight, eps, residual_out, q, scale, _handle(stream))
+    type (bf16 without one) or None; q [T, d] int8 and scale [T] fp32 are written, and values [T, d] bf16 (the
+    codes' values, q * scale) unless None."""
+    bad = (_BINDING or _binding()).add_rmsnorm_i8(x, residual, weight, eps, residual_out, q, scale, values,
+                                                  _handle(stream))
     if bad:
         raise SsdError("ssd_add_rmsnorm_i8", *bad)
 
 
-def ssd_gated_rmsnorm_i8(y, z, weight, eps: float, q, scale, stream=None):
-    """y [T, d] bf16; z [T, d] bf16, dense or a slice of wider rows; weight [d] fp32 or None; q [T, d] int8 and
-    scale [T] fp32 are written."""
-    bad = (_BINDING or _binding()).gated_rmsnorm_i8(y, z, weight, eps, q, scale, _handle(stream))
+def ssd_gated_rmsnorm_i8(y, z, weight, eps: float, q, scale, values=None, stream=None):
+    """y [T, d] bf16; z [T, d] bf16, dense or a slice of wider rows; weight [d] fp32 or None; q, scale and values as
+    in ssd_add_rmsnorm_i8."""
+    bad = (_BINDING or _binding()).gated_rmsnorm_i8(y, z, weight, eps, q, scale, values, _handle(stream))
     if bad:
         raise SsdError("ssd_gated_rmsnorm_i8", *bad)
 

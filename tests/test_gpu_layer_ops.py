@@ -63,7 +63,7 @@ def _check_codes(q, scale, v, weight, eps, gate_err=0.0):
     assert rel.max(initial=0) <= 48 * E + 2 * gate_err, rel.max()
 
 
-NORM_SIZES = [(1, 16), (3, 48), (1, 8192), (130, 2560), (5, 8208), (2, 16400), (2, 32768), (1025, 2048)]
+NORM_SIZES = [(1, 16), (3, 48), (1, 8192), (130, 2560), (5, 8208), (2, 16400), (2, 32768), (1025, 2048), (3001, 512)]
 
 
 @pytest.mark.parametrize("T,d", NORM_SIZES)
@@ -91,10 +91,11 @@ def test_add_rmsnorm(torch_cuda, T, d, residual, weighted, in_place):
     else:
         assert torch.equal(out, (x0.float() + res0.float()).bfloat16())
     _check_codes(host(q), host(scale).astype(np.float64), _np(torch, out), _np(torch, w), 1e-5)
-    if not in_place:                       # without residual_out the codes are the same
-        q2, s2 = torch.empty_like(q), torch.empty_like(scale)
-        iq.ssd_add_rmsnorm_i8(x, res, w, 1e-5, None, q2, s2)
+    if not in_place:                       # without residual_out, and with values, the codes are the same
+        q2, s2, values = torch.empty_like(q), torch.empty_like(scale), torch.full_like(x, float("nan"))
+        iq.ssd_add_rmsnorm_i8(x, res, w, 1e-5, None, q2, s2, values)
         assert torch.equal(q, q2) and torch.equal(scale, s2)
+        assert torch.equal(values, (q.float() * scale[:, None]).bfloat16())
 
 
 @pytest.mark.parametrize("T,d", NORM_SIZES)
@@ -113,6 +114,10 @@ def test_gated_rmsnorm(torch_cuda, T, d, pad):
     zn = _np(torch, z)
     gate_err = (2 * (5 + 1.2 * np.abs(zn).max()) + 1) * E
     _check_codes(host(q), host(scale).astype(np.float64), O.gate(_np(torch, y), zn), _np(torch, w), 1e-5, gate_err)
+    q2, s2, values = torch.empty_like(q), torch.empty_like(scale), torch.full_like(y, float("nan"))
+    iq.ssd_gated_rmsnorm_i8(y, z, w, 1e-5, q2, s2, values=values)
+    assert torch.equal(q, q2) and torch.equal(scale, s2)
+    assert torch.equal(values, (q.float() * scale[:, None]).bfloat16())
 
 
 def test_gate_at_large_arguments(torch_cuda):
@@ -146,21 +151,24 @@ def test_norm_rows_of_zeros_and_rows_that_are_not_finite(torch_cuda, d):
     w = torch.ones(d, device="cuda")
     q = torch.full((8, d), -128, dtype=torch.int8, device="cuda")
     s = torch.full((8,), -7.0, device="cuda")
+    val = torch.empty_like(x)
     z = torch.full((8, d), 20.0, device="cuda").bfloat16()
 
     def check():
         qh, sh = host(q), host(s)
+        vh = host(val.float())
+        assert np.isnan(vh[[2, 3, 4, 6]]).all() and not vh[[1, 5]].any() and np.isfinite(vh[[0, 7]]).all()
         assert not qh[1:7].any()
         assert sh[1] == 1.0 and sh[5] == 1.0 and np.isnan(sh[[2, 3, 4, 6]]).all()
         assert np.abs(qh[0]).max() == 127 and np.abs(qh[7]).max() == 127 and np.isfinite(sh[[0, 7]]).all()
 
-    iq.ssd_add_rmsnorm_i8(x, None, w, 1e-5, None, q, s)
+    iq.ssd_add_rmsnorm_i8(x, None, w, 1e-5, None, q, s, val)
     check()
     q.fill_(-128)
-    iq.ssd_add_rmsnorm_i8(x, torch.zeros(8, d, device="cuda"), w, 1e-5, None, q, s)
+    iq.ssd_add_rmsnorm_i8(x, torch.zeros(8, d, device="cuda"), w, 1e-5, None, q, s, val)
     check()
     q.fill_(-128)
-    iq.ssd_gated_rmsnorm_i8(x, z, w, 1e-5, q, s)
+    iq.ssd_gated_rmsnorm_i8(x, z, w, 1e-5, q, s, val)
     check()
 
 

@@ -13,26 +13,27 @@ OK, INVALID, UNSUPPORTED = 0, 1, 2
 
 def test_add_rmsnorm_refusals():
     f = iq.library().ssd_add_rmsnorm_i8
-    good = [4, 64, F, F, 1, F, 1e-5, F, F, F, None]
+    good = [4, 64, F, F, 1, F, 1e-5, F, F, F, None, None]
     for i, v, want in [(0, -1, INVALID), (1, 0, INVALID), (1, 40, UNSUPPORTED), (1, 32784, UNSUPPORTED),
                        (2, None, INVALID), (2, ODD, INVALID), (3, ODD, INVALID), (3, None, INVALID),
                        (5, ODD, INVALID), (6, 0.0, INVALID), (6, -1.0, INVALID), (6, float("nan"), INVALID),
-                       (7, ODD, INVALID), (8, None, INVALID), (8, ODD, INVALID), (9, None, INVALID)]:
+                       (7, ODD, INVALID), (8, None, INVALID), (8, ODD, INVALID), (9, None, INVALID), (10, ODD, INVALID)]:
         a = list(good)
         a[i] = v
         assert f(*a) == want, (i, v)
-    assert f(0, 64, None, None, 0, None, 1e-5, None, None, None, None) == OK      # no tokens
+    assert f(0, 64, None, None, 0, None, 1e-5, None, None, None, None, None) == OK      # no tokens
 
 
 def test_gated_rmsnorm_refusals():
     f = iq.library().ssd_gated_rmsnorm_i8
-    good = [4, 64, F, F, 96, F, 1e-5, F, F, None]
+    good = [4, 64, F, F, 96, F, 1e-5, F, F, None, None]
     for i, v, want in [(0, -1, INVALID), (1, 24, UNSUPPORTED), (2, None, INVALID), (3, None, INVALID), (3, ODD, INVALID),
-                       (4, 56, INVALID), (4, 100, INVALID), (6, 0.0, INVALID), (7, None, INVALID), (8, ODD, INVALID)]:
+                       (4, 56, INVALID), (4, 100, INVALID), (6, 0.0, INVALID), (7, None, INVALID), (8, ODD, INVALID),
+                       (9, ODD, INVALID)]:
         a = list(good)
         a[i] = v
         assert f(*a) == want, (i, v)
-    assert f(0, 64, None, None, 64, None, 1e-5, None, None, None) == OK
+    assert f(0, 64, None, None, 64, None, 1e-5, None, None, None, None) == OK
 
 
 def test_matmul_refusals():
