@@ -227,12 +227,11 @@ def _own(s):
     import int8_quant_b200 as iq
     op = s["case"]["op"]
     if op == "add_norm":
-        iq.ssd_add_rmsnorm_i8(s["x"], s["residual"], s["weight"], EPS, s["residual_out"], s["codes"], s["scale"])
-        torch.mul(s["codes"], s["scale"][:, None], out=s["value"])
+        iq.ssd_add_rmsnorm_i8(s["x"], s["residual"], s["weight"], EPS, s["residual_out"], s["codes"], s["scale"],
+                              s["value"])
         return {"value": s["value"], "scale": s["scale"], "residual": s["residual_out"]}
     if op == "gate_norm":
-        iq.ssd_gated_rmsnorm_i8(s["y"], s["z"], s["weight"], EPS, s["codes"], s["scale"])
-        torch.mul(s["codes"], s["scale"][:, None], out=s["value"])
+        iq.ssd_gated_rmsnorm_i8(s["y"], s["z"], s["weight"], EPS, s["codes"], s["scale"], s["value"])
         return {"value": s["value"], "scale": s["scale"]}
     if op == "matmul":
         iq.ssd_matmul_i8(s["q"], s["s_t"], s["Wq"], s["s_w"], s["bias"], s["out"], s["status"])
