@@ -7,8 +7,13 @@
 // conv_fwd_kernel: a CTA stages a tile of kTile tokens (and the W-1 in front of them) of 256
 // channels in shared memory with cp.async, then each thread slides the window along half the
 // tile's tokens for 4 channels.  Bound by HBM (2 bytes read, 2 written per channel and token);
-// loads wait in shared memory, not in registers, so 8 CTAs of 128 threads an SM keep 140 KB
-// of them in flight.  Blocks behind those of the convolution form dt and the final state.
+// loads wait in shared memory, not in registers, so 6 CTAs of 128 threads an SM keep 200 KB
+// of them in flight.  8 rows of 8192 tokens of 5376 channels, and 80 dt: 1.44 GB in 227 us
+// (6.3 TB/s; 6.5 is the copy bandwidth), 257 us once the power limit has lowered the clock to
+// 1.6 GHz.  Tiles of 32 tokens (more halo, more parameter loads) take 239 and 280 us, of 128
+// (3 CTAs an SM) 251 and 274; plain instead of packed fp32 arithmetic 258 and 283; a window
+// slid along registers, without the staging, 344.  Blocks behind those of the convolution form
+// dt and the final state.
 // conv_step_kernel: one token; a thread owns 8 channels of a batch row and shifts their
 // state in place.
 #include "kernels.h"
@@ -19,7 +24,7 @@ namespace {
 
 constexpr int kStepThreads = 256;
 constexpr int kThreads = 128;               // of conv_fwd_kernel
-constexpr int kTile = 32;                   // its tokens
+constexpr int kTile = 64;                   // its tokens
 constexpr int kBlock = 256;                 // its channels
 constexpr int kCh = 4;                      // channels of a thread
 constexpr int kGroups = kBlock / kCh, kSubs = kThreads / kGroups, kSub = kTile / kSubs;
@@ -140,7 +145,7 @@ __device__ __forceinline__ void conv_tile(const ConvArgs& a) {
         col += (W - 1) * kRow;
     }
     if (n >= kSub) {
-#pragma unroll
+#pragma unroll 8
         for (int j = 0; j < kSub; ++j, out += stride)
             *reinterpret_cast<uint2*>(out) = conv_token<W>(col[j * kRow], w, bias, h);
     } else {

@@ -13,7 +13,8 @@
 // the gate, 2 more where the codes' values are asked for.  One CTA per token and VPT vectors
 // of 8 features a thread, all loads issued before anything else; many small CTAs resident on
 // an SM cover each other's barrier.  Measured, in a graph (6.53 TB/s is the copy bandwidth):
-//   65536 x 2560, fp32 residual   268 us = 6.9 TB/s       16384 x 5120, gate   80 us = 5.2 TB/s
+//   65536 x 2560, fp32 residual   266 us = 6.9 TB/s, with values 318 us = 6.9 TB/s
+//   16384 x 5120, gate             80 us = 5.2 TB/s, with values  96 us = 6.1 TB/s
 // The gate spends two special-function instructions a feature (exponential, reciprocal); with
 // packed fp32 arithmetic it takes half the instructions of the plain form (95 us).  A
 // persistent grid that loads the next token ahead needs twice the registers and was slower:
@@ -70,17 +71,16 @@ __device__ __forceinline__ float warp_sum(float v) {
     for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
     return v;
 }
+// The largest of a warp's values, none of them negative (their bits are in their order).
 __device__ __forceinline__ float warp_max(float v) {
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, off));
-    return v;
+    return __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(v)));
 }
 
 // 64 registers up to four vectors a thread: 1024 threads an SM
 template <int KIND, int VPT>
 __global__ void __launch_bounds__(kMaxThreads, VPT == 8 ? 1 : 2)
 rmsnorm_i8_kernel(const __grid_constant__ NormArgs a) {
-    __shared__ float2 part[kMaxThreads / 32];
+    __shared__ float2 part[kMaxThreads / 32], row_scale;
     const int nv = a.d >> 3, warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nw = blockDim.x >> 5;
     const float inf = __int_as_float(0x7f800000);
     const long long row = blockIdx.x;
@@ -138,17 +138,24 @@ rmsnorm_i8_kernel(const __grid_constant__ NormArgs a) {
     top = warp_max(top);
     if (lane == 0) part[warp] = make_float2(ss, top);
     __syncthreads();
-    const float2 mine = lane < nw ? part[lane] : make_float2(0.f, 0.f);
-    ss = warp_sum(mine.x);
-    top = warp_max(mine.y);
-    // A row that is not finite gets the scale NaN and codes 0; a row of zeros (below 2^-100,
-    // where 127 / top would overflow) the scale 1 and codes 0.
-    const bool finite = ss < inf && top < inf;
-    const bool some = finite && top >= 0x1p-100f;
-    const float inv = some ? 127.0f / top : 0.f;
-    const float scale = some ? top * rsqrtf(ss / (float)a.d + a.eps) / 127.0f
+    // One warp finishes the reduction.  A row that is not finite gets the scale NaN and codes
+    // 0; a row of zeros (below 2^-100, where 127 / top would overflow) the scale 1 and codes 0.
+    if (warp == 0) {
+        const float2 mine = lane < nw ? part[lane] : make_float2(0.f, 0.f);
+        ss = warp_sum(mine.x);
+        top = warp_max(mine.y);
+        const bool finite = ss < inf && top < inf;
+        const bool some = finite && top >= 0x1p-100f;
+        const float s = some ? top * rsqrtf(ss / (float)a.d + a.eps) / 127.0f
                              : finite ? 1.0f : __int_as_float(0x7fffffff);
-    if (threadIdx.x == 0) a.scale[row] = scale;
+        if (lane == 0) {
+            a.scale[row] = s;
+            row_scale = make_float2(some ? 127.0f / top : 0.f, s);
+        }
+    }
+    __syncthreads();
+    const float inv = row_scale.x, scale = row_scale.y;
+    const bool some = inv != 0.f;
 #pragma unroll
     for (int k = 0; k < VPT; ++k) {
         const int i = threadIdx.x + k * blockDim.x;
