@@ -4,16 +4,15 @@
 // the sum exact in INT32 on the tensor cores (tcgen05.mma kind::i8, operands by TMA with the
 // 128-byte swizzle in K slices of 128; what lies outside the matrices arrives as zeros).
 //
-// In both kernels the MMA's rows (TMEM lanes) are output channels and its columns tokens, so
-// a thread of the epilogue owns a channel: its scale and bias stay in registers, and a warp
-// stores 32 consecutive channels of a token at a time, 64 contiguous bytes whatever n's
-// alignment.
-//
 //   matmul_pair_kernel  many tokens: a CTA pair (cta_group::2) per 256 x 256 output tile,
-//                       persistent, a 6-stage ring, two accumulators.
-//   matmul_few_kernel   few tokens or few tiles: one 128-channel tile of up to 128 tokens
-//                       per cluster, the K axis split over the cluster's CTAs and the
-//                       INT32 partial sums joined through distributed shared memory.
+//                       persistent, a ring of K slices, two accumulators.  Its rows (TMEM
+//                       lanes) are tokens and its columns channels where n % 8 == 0: tiles
+//                       leave through shared memory by TMA.  Otherwise no row of the output
+//                       is aligned, and the rows are channels: a warp stores 32 channels
+//                       of a token at a time, 64 contiguous bytes whatever their alignment.
+//   matmul_few_kernel   few tokens or few tiles: one 128-channel tile (rows) of up to 128
+//                       tokens per cluster, the K axis split over the cluster's CTAs and
+//                       the INT32 partial sums joined through distributed shared memory.
 //
 // Every wait is bounded; an expired wait raises the CTA's abort flag and records
 // SSD_ERR_TIMEOUT in the status word.
@@ -25,7 +24,8 @@ namespace ssd {
 namespace {
 
 constexpr int kBK = 128;                              // K slice: one 128-byte swizzled row
-constexpr int kWarps = 6;                             // 0 TMA, 1 MMA, 2-5 epilogue
+constexpr int kWarps = 10;                            // 0 TMA, 1 MMA, 2-9 epilogue
+constexpr int kEpi = 8;                               // epilogue warps: two per TMEM lane quarter, half the columns each
 constexpr long long kDrainLimit = 400000000LL;        // cycles an aborting CTA waits for its copies and MMAs
 
 struct MatmulArgs {
@@ -38,29 +38,6 @@ struct MatmulArgs {
     int* status;
 };
 
-// 32 columns (tokens t0 ..) of this thread's channel: scale and store.  `dst` points at token
-// t0's element; `live` tokens of the 32 exist.
-__device__ __forceinline__ void store_tokens(const uint32_t (&v)[32], const float* __restrict__ s_t, float sw,
-                                             float bias, uint16_t* dst, long long N, int live) {
-    if (live >= 32) {
-#pragma unroll
-        for (int j = 0; j < 32; ++j) {
-            const float f = fmaf((float)(int)v[j] * sw, __ldg(s_t + j), bias);
-            *dst = float_to_bf16_bits(f);
-            dst += N;
-        }
-    } else {
-#pragma unroll
-        for (int j = 0; j < 32; ++j) {
-            if (j < live) {
-                const float f = fmaf((float)(int)v[j] * sw, __ldg(s_t + j), bias);
-                *dst = float_to_bf16_bits(f);
-                dst += N;
-            }
-        }
-    }
-}
-
 // ---------------------------------------------------------------- many tokens: CTA pairs
 
 namespace pair {
@@ -69,7 +46,10 @@ constexpr int kRows = 128;                            // rows of each operand pe
 constexpr int kTile = 2 * kRows;
 constexpr int kStages = 6, kAcc = 2;
 constexpr int kOpBytes = kRows * kBK;
-constexpr int OFF_A = 0, OFF_B = kStages * kOpBytes, OFF_BAR = 2 * kStages * kOpBytes;
+constexpr int kOutBytes = 32 * 64;                   // a warp's 32 rows of 32 bf16 columns, on their way out
+constexpr int OFF_A = 0, OFF_B = kStages * kOpBytes, OFF_OUT = 2 * kStages * kOpBytes;
+constexpr int OFF_COL = OFF_OUT + kEpi * kOutBytes;   // [kAcc][2][kTile] fp32: the columns' scales and biases
+constexpr int OFF_BAR = OFF_COL + kAcc * 2 * kTile * 4;
 constexpr int B_FULL = 0, B_EMPTY = kStages, B_AFULL = 2 * kStages, B_AEMPTY = B_AFULL + kAcc,
               B_DRAIN = B_AEMPTY + kAcc, NBAR = B_DRAIN + 1;
 constexpr int OFF_FLAG = OFF_BAR + NBAR * 8, OFF_TMEM = OFF_FLAG + 8, SMEM = OFF_TMEM + 8;
@@ -87,9 +67,41 @@ __device__ __forceinline__ void tile_at(const MatmulArgs& p, long long t, int* n
     *n0 = (r / in) * kTile;
 }
 
+// 32 columns of this thread's row (token), scaled and rounded, into its 64 bytes of `buf`
+// (32 such rows, 64-byte swizzle).
+__device__ __forceinline__ void fill_box(const uint32_t (&v)[32], float st, const float* sw, const float* bias,
+                                         uint8_t* buf, int lane) {
+    const f32x2 st2 = both2(st);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        uint32_t o[4];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int c = 8 * j + 4 * e;
+            const float4 w = *reinterpret_cast<const float4*>(sw + c), b = *reinterpret_cast<const float4*>(bias + c);
+            const f32x2 x = mul2(pair2((float)(int)v[c], (float)(int)v[c + 1]), pair2(w.x, w.y));
+            const f32x2 y = mul2(pair2((float)(int)v[c + 2], (float)(int)v[c + 3]), pair2(w.z, w.w));
+            o[2 * e] = pack2(fma2(x, st2, pair2(b.x, b.y)));
+            o[2 * e + 1] = pack2(fma2(y, st2, pair2(b.z, b.w)));
+        }
+        *reinterpret_cast<uint4*>(buf + lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+    }
+}
+
+// 32 columns (tokens) of this thread's channel.  `dst`: the first token's element; `live` of
+// the tokens exist.
+__device__ __forceinline__ void store_tokens(const uint32_t (&v)[32], const float* __restrict__ s_t, float sw,
+                                             float bias, uint16_t* dst, long long N, int live) {
+#pragma unroll
+    for (int j = 0; j < 32; ++j)
+        if (j < live) dst[j * N] = float_to_bf16_bits(fmaf((float)(int)v[j] * sw, __ldg(s_t + j), bias));
+}
+
+// SWAP: the tile's rows are channels (tm_a: the weights), its columns tokens.
+template <bool SWAP>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWarps * 32, 1)
-matmul_pair_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_q,
-                   const __grid_constant__ MatmulArgs p) {
+matmul_pair_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
+                   const __grid_constant__ CUtensorMap tm_out, const __grid_constant__ MatmulArgs p) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* sm = smem_raw + ((1024u - (tc::smem_u32(smem_raw) & 1023u)) & 1023u);
     uint64_t* bar = reinterpret_cast<uint64_t*>(sm + OFF_BAR);
@@ -102,8 +114,8 @@ matmul_pair_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_consta
     const long long tiles = (long long)p.tiles_t * p.tiles_n;
     const int pairs = gridDim.x >> 1, me = blockIdx.x >> 1;
     if (threadIdx.x == 0) {
-        // an accumulator is free once the four epilogue warps of both CTAs have read it
-        for (int i = 0; i < NBAR; ++i) tc::mbar_init(bar + i, i >= B_AEMPTY && i < B_DRAIN ? 8 : 1);
+        // an accumulator is free once the epilogue warps of both CTAs have read it
+        for (int i = 0; i < NBAR; ++i) tc::mbar_init(bar + i, i >= B_AEMPTY && i < B_DRAIN ? 2 * kEpi : 1);
         *abort_flag = 0;
         tc::fence_mbar_init();
     }
@@ -119,37 +131,43 @@ matmul_pair_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_consta
 
     if (warp == 0) {
         if (lane == 0) {
-            tc::prefetch_tmap(&tm_w);
-            tc::prefetch_tmap(&tm_q);
-            long long kc = 0;                                     // K slices issued so far (ring position)
+            tc::prefetch_tmap(&tm_a);
+            tc::prefetch_tmap(&tm_b);
+            int s = 0;
+            uint32_t phase = 1;                                   // a fresh stage counts as free
+            int issued = 0;                                       // stages with a copy issued (up to kStages)
             bool ok = true;
             for (long long t = me; ok && t < tiles; t += pairs) {
                 int n0, t0;
                 tile_at(p, t, &n0, &t0);
-                n0 += (int)rank * kRows;
-                t0 += (int)rank * kRows;
-                for (int k = 0; k < nk; ++k, ++kc) {
-                    const int s = (int)(kc % kStages);
-                    if (!(ok = tc::wait_or_abort(bar + B_EMPTY + s, (((uint32_t)(kc / kStages)) & 1) ^ 1, abort_flag,
-                                                 p.status, kStatusTimeout)))
-                        break;
+                const int a0 = (SWAP ? n0 : t0) + (int)rank * kRows, b0 = (SWAP ? t0 : n0) + (int)rank * kRows;
+                for (int k = 0; k < nk; ++k) {
+                    if (!(ok = tc::wait_or_abort(bar + B_EMPTY + s, phase, abort_flag, p.status, kStatusTimeout))) break;
                     // both CTAs' loads of a stage count on the even CTA's barrier
                     if (leader) tc::mbar_arrive_expect_tx(bar + B_FULL + s, 4 * kOpBytes);
                     const uint32_t full = tc::map_rank(tc::smem_u32(bar + B_FULL + s), 0);
-                    tc::tma_load_2d_pair(sm + OFF_A + s * kOpBytes, &tm_w, full, k * kBK, n0);
-                    tc::tma_load_2d_pair(sm + OFF_B + s * kOpBytes, &tm_q, full, k * kBK, t0);
+                    tc::tma_load_2d_pair(sm + OFF_A + s * kOpBytes, &tm_a, full, k * kBK, a0);
+                    tc::tma_load_2d_pair(sm + OFF_B + s * kOpBytes, &tm_b, full, k * kBK, b0);
+                    if (issued < kStages) ++issued;
+                    if (++s == kStages) {
+                        s = 0;
+                        phase ^= 1;
+                    }
                 }
             }
             if (!ok && leader)                                    // the copies in flight land before the CTA ends
-                for (long long j = kc > kStages ? kc - kStages : 0; j < kc; ++j)
-                    tc::mbar_wait(bar + B_FULL + j % kStages, ((uint32_t)(j / kStages)) & 1, kDrainLimit);
+                for (int i = 0; i < issued; ++i) {
+                    // the phase of stage s's latest copy is the one before the free phase waited for next
+                    const int st = (s + kStages - 1 - i) % kStages;
+                    tc::mbar_wait(bar + B_FULL + st, st < s ? phase ^ 1 : phase, kDrainLimit);
+                }
         }
         __syncwarp();
     } else if (warp == 1) {
         if (leader) {
             const uint32_t idesc = tc::idesc_s8_s32(kTile, kTile, tc::kMajorK, tc::kMajorK);
-            long long kc = 0;
-            int it = 0;                                           // tiles of this pair so far
+            int s = 0, it = 0;                                    // ring position; tiles of this pair so far
+            uint32_t phase = 0;
             bool ok = true;
             for (long long t = me; ok && t < tiles; t += pairs, ++it) {
                 const int a = it & 1;
@@ -159,10 +177,9 @@ matmul_pair_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_consta
                 if (!ok) break;
                 tc::tc_fence_after();
                 const uint32_t dacc = tmem + (uint32_t)(a * kTile);
-                for (int k = 0; k < nk; ++k, ++kc) {
-                    const int s = (int)(kc % kStages);
-                    ok = __all_sync(0xffffffffu, tc::wait_or_abort(bar + B_FULL + s, ((uint32_t)(kc / kStages)) & 1,
-                                                                  abort_flag, p.status, kStatusTimeout));
+                for (int k = 0; k < nk; ++k) {
+                    ok = __all_sync(0xffffffffu, tc::wait_or_abort(bar + B_FULL + s, phase, abort_flag, p.status,
+                                                                  kStatusTimeout));
                     if (!ok) break;
                     tc::tc_fence_after();
                     if (tc::elect_one()) {
@@ -176,6 +193,10 @@ matmul_pair_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_consta
                         if (k == nk - 1) tc::mma_commit_pair(bar + B_AFULL + a);
                     }
                     __syncwarp();
+                    if (++s == kStages) {
+                        s = 0;
+                        phase ^= 1;
+                    }
                 }
             }
             if (!ok) {                                            // the MMAs in flight end before TMEM is freed
@@ -185,43 +206,100 @@ matmul_pair_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_consta
             }
         }
     } else {
-        // epilogue: warp w reads TMEM lanes 32 (w % 4) .. +31, channels n0 + 128 rank + 32 (w % 4) + lane
-        const int quarter = warp & 3;
+        // epilogue: warp w reads TMEM lanes 32 (w % 4) .. +31, the tile's rows 128 rank + 32 (w % 4) + lane,
+        // and columns half .. half + 127
+        const int quarter = warp & 3, half = (warp - 2) / 4 * kRows;
+        uint8_t* out_buf = sm + OFF_OUT + (warp - 2) * kOutBytes;
         int it = 0;
+        // scales (and biases) of a tile are loaded while the one before it is worked on
+        float srow = 0.f, brow = 0.f, ccol = 0.f, bcol = 0.f;
+        const auto load_scales = [&](long long t) {
+            int n0, t0;
+            if (t >= tiles) return;
+            tile_at(p, t, &n0, &t0);
+            const int row = (SWAP ? n0 : t0) + (int)rank * kRows + quarter * 32 + lane;
+            const int c = n0 + half + quarter * 32 + lane;
+            const bool in = row < (SWAP ? p.N : p.T);
+            srow = in ? __ldg((SWAP ? p.s_w : p.s_t) + row) : 0.f;
+            brow = SWAP && in && p.bias ? __ldg(p.bias + row) : 0.f;
+            ccol = !SWAP && c < p.N ? __ldg(p.s_w + c) : 0.f;
+            bcol = !SWAP && c < p.N && p.bias ? __ldg(p.bias + c) : 0.f;
+        };
+        load_scales(me);
         for (long long t = me; t < tiles; t += pairs, ++it) {
             const int a = it & 1;
             int n0, t0;
             tile_at(p, t, &n0, &t0);
-            const int ch = n0 + (int)rank * kRows + quarter * 32 + lane;
-            const bool in = ch < p.N;
-            const float sw = in ? __ldg(p.s_w + ch) : 0.f;
-            const float bias = in && p.bias ? __ldg(p.bias + ch) : 0.f;
-            const uint32_t trow = tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(a * kTile);
+            const int row0 = (SWAP ? n0 : t0) + (int)rank * kRows + quarter * 32;
+            const float st = srow, sb = brow;
+            float* col = reinterpret_cast<float*>(sm + OFF_COL) + a * 2 * kTile;
+            if (!SWAP) {
+                // the channels' scales and biases, for every warp; the other half of the buffer
+                // may still be read by a warp that is one tile behind
+                col[half + quarter * 32 + lane] = ccol;
+                col[kTile + half + quarter * 32 + lane] = bcol;
+                tc::named_sync(1, kEpi * 32);
+            }
+            load_scales(t + pairs);
+            const uint32_t trow = tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(a * kTile + half);
             const bool ok = tc::wait_or_abort(bar + B_AFULL + a, ((uint32_t)(it >> 1)) & 1, abort_flag, p.status,
                                               kStatusTimeout);
-            if (!__all_sync(0xffffffffu, ok)) break;
+            // the warps stay together: the named barrier above counts all of them
+            if (!(SWAP ? __all_sync(0xffffffffu, ok) : tc::named_and(2, kEpi * 32, ok))) break;
             tc::tc_fence_after();
-            uint16_t* dst = p.out + (long long)t0 * p.N + ch;
-            for (int c = 0; c < kTile / 32; ++c, dst += 32LL * p.N) {
-                uint32_t v[32];
-                tc::tmem_ld32(trow + c * 32, v);
-                tc::tmem_wait_ld();
-                if (c == kTile / 32 - 1) {
-                    // the whole accumulator is in registers: hand it back to the MMA warp
-                    tc::tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) tc::mbar_arrive_cluster(tc::map_rank(tc::smem_u32(bar + B_AEMPTY + a), 0));
+            // this warp's part of the accumulator to registers, and the accumulator back to the MMA warp
+            uint32_t v[4][32];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) tc::tmem_ld32(trow + i * 32, v[i]);
+            tc::tmem_wait_ld();
+            tc::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive_cluster(tc::map_rank(tc::smem_u32(bar + B_AEMPTY + a), 0));
+            if (SWAP) {
+                const int row = row0 + lane;
+                if (row < p.N) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int c = t0 + half + i * 32;
+                        store_tokens(v[i], p.s_t + c, st, sb, p.out + (long long)c * p.N + row, p.N, p.T - c);
+                    }
                 }
-                const int live = p.T - t0 - c * 32;
-                if (in) store_tokens(v, p.s_t + t0 + c * 32, sw, bias, dst, p.N, live);
+            } else if (row0 < p.T && n0 + half < p.N) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int c = half + i * 32;
+                    if (n0 + c >= p.N) break;
+                    if (lane == 0) tc::tma_store_wait_read0();    // the box before has left the buffer
+                    __syncwarp();
+                    fill_box(v[i], st, col + c, col + kTile + c, out_buf, lane);
+                    tc::fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        tc::tma_store_2d(&tm_out, out_buf, n0 + c, row0);
+                        tc::tma_store_commit();
+                    }
+                }
             }
         }
+        if (!SWAP && lane == 0) tc::tma_store_wait0();            // the stores have read shared memory and are done
         __syncwarp();
     }
     tc::tc_fence_before();
     __syncthreads();
     tc::cluster_sync();                                           // no CTA leaves while the other may reach it
     if (warp == 1) tc::tmem_dealloc_pair(tmem, kAcc * kTile);
+}
+
+template <bool SWAP>
+cudaError_t launch(const CUtensorMap& mq, const CUtensorMap& mw, const CUtensorMap& mo, const MatmulArgs& p,
+                   cudaStream_t st) {
+    const int smem = SMEM + 1024;
+    const cudaError_t e = cudaFuncSetAttribute(matmul_pair_kernel<SWAP>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    const long long tiles = (long long)p.tiles_t * p.tiles_n;
+    const int most = device_sm_count() / 2, pairs = tiles < most ? (int)tiles : most;
+    matmul_pair_kernel<SWAP><<<2 * pairs, kWarps * 32, smem, st>>>(SWAP ? mw : mq, SWAP ? mq : mw, mo, p);
+    return cudaGetLastError();
 }
 
 }  // namespace pair
@@ -231,17 +309,20 @@ matmul_pair_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_consta
 namespace few {
 
 constexpr int kRows = 128;                            // channels of a tile
-constexpr int kMaxStages = 6;
+constexpr int kMaxStages = 12;
+constexpr int kBudget = 98304;                        // shared memory for stages: two CTAs an SM
 constexpr int B_FULL = 0, B_EMPTY = kMaxStages, B_DONE = 2 * kMaxStages, NBAR = B_DONE + 1;
+constexpr int OFF_FLAG = NBAR * 8, OFF_TMEM = OFF_FLAG + 8, OFF_BUF = 1024;
+static_assert(OFF_TMEM + 8 <= OFF_BUF, "barriers in front of the stages");
 
 template <int BN>
 struct Layout {
     static constexpr int A_BYTES = kRows * kBK, B_BYTES = BN * kBK, STAGE = A_BYTES + B_BYTES;
     static constexpr int RED = BN * kRows * 4;                    // partial sums, over the stages
-    static constexpr int STAGES = 98304 / STAGE < kMaxStages ? 98304 / STAGE : kMaxStages;
-    static constexpr int BUF = STAGES * STAGE > RED ? STAGES * STAGE : RED;
-    static constexpr int OFF_BAR = BUF, OFF_FLAG = OFF_BAR + NBAR * 8, OFF_TMEM = OFF_FLAG + 8, SMEM = OFF_TMEM + 8;
+    static constexpr int MOST = kBudget / STAGE < kMaxStages ? kBudget / STAGE : kMaxStages;
     static constexpr int COLS = BN < 32 ? 32 : BN;                // TMEM columns
+    // with `stages` of them, and room to align the first
+    static int smem(int stages) { return 1024 + OFF_BUF + (stages * STAGE > RED ? stages * STAGE : RED); }
 };
 
 // Cluster rank r takes the K slices [r nk / S, (r + 1) nk / S) of the tile (channels n0 ..,
@@ -250,23 +331,32 @@ struct Layout {
 template <int BN>
 __global__ void __launch_bounds__(kWarps * 32)
 matmul_few_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_q,
-                  const __grid_constant__ MatmulArgs p, int S) {
+                  const __grid_constant__ MatmulArgs p, int S, int stages) {
     using Ly = Layout<BN>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* sm = smem_raw + ((1024u - (tc::smem_u32(smem_raw) & 1023u)) & 1023u);
-    uint64_t* bar = reinterpret_cast<uint64_t*>(sm + Ly::OFF_BAR);
-    volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + Ly::OFF_FLAG);
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + Ly::OFF_TMEM);
+    uint64_t* bar = reinterpret_cast<uint64_t*>(sm);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + OFF_FLAG);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + OFF_TMEM);
+    uint8_t* buf = sm + OFF_BUF;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int rank = (int)tc::cluster_rank();
+    const int rank = S > 1 ? (int)tc::cluster_rank() : 0;
     const int tile = blockIdx.x / S;
     const int n0 = (tile % p.tiles_n) * kRows, t0 = (tile / p.tiles_n) * BN;
     const int nk = (p.K + kBK - 1) / kBK;
     const int k0 = (int)((long long)rank * nk / S), k1 = (int)((long long)(rank + 1) * nk / S);
+    const int first = min(stages, k1 - k0);                       // slices loaded before anything waits
+    const auto load = [&](int j, int s) {
+        tc::mbar_arrive_expect_tx(bar + B_FULL + s, Ly::STAGE);
+        tc::tma_load_2d(buf + s * Ly::STAGE, &tm_w, bar + B_FULL + s, (k0 + j) * kBK, n0);
+        tc::tma_load_2d(buf + s * Ly::STAGE + Ly::A_BYTES, &tm_q, bar + B_FULL + s, (k0 + j) * kBK, t0);
+    };
     if (threadIdx.x == 0) {
         for (int i = 0; i < NBAR; ++i) tc::mbar_init(bar + i, 1);
         *abort_flag = 0;
         tc::fence_mbar_init();
+        tc::fence_proxy_async_smem();
+        for (int j = 0; j < first; ++j) load(j, j);
     }
     if (warp == 1) {
         tc::tmem_alloc(tmem_slot, Ly::COLS);
@@ -280,32 +370,32 @@ matmul_few_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constan
     bool ok = true;
     if (warp == 0) {
         if (lane == 0) {
-            int k = k0;
-            for (; k < k1; ++k) {
-                const int j = k - k0, s = j % Ly::STAGES;
-                if (!(ok = tc::wait_or_abort(bar + B_EMPTY + s, (((uint32_t)(j / Ly::STAGES)) & 1) ^ 1, abort_flag,
-                                             p.status, kStatusTimeout)))
-                    break;
-                uint8_t* st = sm + s * Ly::STAGE;
-                tc::mbar_arrive_expect_tx(bar + B_FULL + s, Ly::STAGE);
-                tc::tma_load_2d(st, &tm_w, bar + B_FULL + s, k * kBK, n0);
-                tc::tma_load_2d(st + Ly::A_BYTES, &tm_q, bar + B_FULL + s, k * kBK, t0);
+            int j = first, s = 0;
+            uint32_t phase = 0;                                   // of the stage's previous use
+            for (; j < k1 - k0; ++j) {
+                if (!(ok = tc::wait_or_abort(bar + B_EMPTY + s, phase, abort_flag, p.status, kStatusTimeout))) break;
+                load(j, s);
+                if (++s == stages) {
+                    s = 0;
+                    phase ^= 1;
+                }
             }
-            if (!ok)
-                for (int j = max(0, k - k0 - Ly::STAGES); j < k - k0; ++j)
-                    tc::mbar_wait(bar + B_FULL + j % Ly::STAGES, ((uint32_t)(j / Ly::STAGES)) & 1, kDrainLimit);
+            if (!ok)                                              // the copies in flight land before the CTA ends
+                for (int i = max(0, j - stages); i < j; ++i)
+                    tc::mbar_wait(bar + B_FULL + i % stages, ((uint32_t)(i / stages)) & 1, kDrainLimit);
         }
         __syncwarp();
     } else if (warp == 1) {
         const uint32_t idesc = tc::idesc_s8_s32(kRows, BN, tc::kMajorK, tc::kMajorK);
-        for (int k = k0; ok && k < k1; ++k) {
-            const int j = k - k0, s = j % Ly::STAGES;
-            ok = __all_sync(0xffffffffu, tc::wait_or_abort(bar + B_FULL + s, ((uint32_t)(j / Ly::STAGES)) & 1,
-                                                          abort_flag, p.status, kStatusTimeout));
+        int s = 0;
+        uint32_t phase = 0;
+        for (int j = 0; j < k1 - k0; ++j) {
+            ok = __all_sync(0xffffffffu, tc::wait_or_abort(bar + B_FULL + s, phase, abort_flag, p.status,
+                                                          kStatusTimeout));
             if (!ok) break;
             tc::tc_fence_after();
             if (tc::elect_one()) {
-                const uint8_t* st = sm + s * Ly::STAGE;
+                const uint8_t* st = buf + s * Ly::STAGE;
                 const uint64_t da = tc::smem_desc(tc::smem_u32(st), 16, 1024, tc::kLayoutSw128);
                 const uint64_t db = tc::smem_desc(tc::smem_u32(st + Ly::A_BYTES), 16, 1024, tc::kLayoutSw128);
 #pragma unroll
@@ -314,54 +404,100 @@ matmul_few_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constan
                 tc::mma_commit(bar + B_EMPTY + s);
             }
             __syncwarp();
+            if (++s == stages) {
+                s = 0;
+                phase ^= 1;
+            }
         }
         if (tc::elect_one()) tc::mma_commit(bar + B_DONE);          // every MMA issued, also when the loop gave up
         __syncwarp();
         if (!ok) tc::mbar_wait(bar + B_DONE, 0, kDrainLimit);
     }
-    const int quarter = warp & 3, row = quarter * 32 + lane, ch = n0 + row;
-    const bool in = ch < p.N;
+    const int quarter = warp & 3, row = quarter * 32 + lane, ch = n0 + row, part = (warp - 2) / 4;
+    const bool in = warp >= 2 && ch < p.N;
     const float sw = in ? __ldg(p.s_w + ch) : 0.f;
     const float bias = in && p.bias ? __ldg(p.bias + ch) : 0.f;
     const int live = min(BN, p.T - t0);
-    int* red = reinterpret_cast<int*>(sm);
+    int* red = reinterpret_cast<int*>(buf);
     if (warp >= 2) {
-        // thread = channel: partial sums to shared memory, a token's 128 channels in a row
         ok = __all_sync(0xffffffffu, tc::wait_or_abort(bar + B_DONE, 0, abort_flag, p.status, kStatusTimeout));
         tc::tc_fence_after();
+        const uint32_t trow = tmem + ((uint32_t)(quarter * 32) << 16);
+        uint16_t* dst = p.out + (long long)t0 * p.N + ch;
         if (ok) {
-            const uint32_t trow = tmem + ((uint32_t)(quarter * 32) << 16);
+            // thread = channel: partial sums to shared memory, a token's 128 channels in a row;
+            // a CTA on its own stores what it has
 #pragma unroll 1
-            for (int c = 0; c < BN; c += 16) {
+            for (int c = 16 * part; c < live; c += 32) {
                 uint32_t v[16];
                 tc::tmem_ld16(trow + c, v);
                 tc::tmem_wait_ld();
+                if (S > 1) {
 #pragma unroll
-                for (int j = 0; j < 16; ++j) red[(c + j) * kRows + row] = (int)v[j];
+                    for (int j = 0; j < 16; ++j) red[(c + j) * kRows + row] = (int)v[j];
+                } else if (in) {
+#pragma unroll
+                    for (int j = 0; j < 16; ++j)
+                        if (c + j < live)
+                            dst[(long long)(c + j) * p.N] = float_to_bf16_bits(
+                                fmaf((float)(int)v[j] * sw, __ldg(p.s_t + t0 + c + j), bias));
+                }
             }
         }
     }
     tc::tc_fence_before();
     __syncthreads();
-    tc::cluster_sync();
-    if (warp >= 2 && ok && in) {
-        const uint32_t mine = tc::smem_u32(red + row);
-        uint16_t* dst = p.out + (long long)t0 * p.N + ch;
-        for (int j = rank; j < live; j += S) {
-            int sum = 0;
-            for (int r = 0; r < S; ++r) sum += tc::ld_cluster_s32(tc::map_rank(mine + j * kRows * 4, r));
-            dst[(long long)j * p.N] = float_to_bf16_bits(fmaf((float)sum * sw, __ldg(p.s_t + t0 + j), bias));
+    if (S > 1) {
+        tc::cluster_sync();
+        if (warp >= 2 && ok) {
+            // a warp takes a token of this rank's share, a lane four channels
+            const int c4 = n0 + 4 * lane;
+            const uint32_t mine = tc::smem_u32(red) + 16u * lane;
+            float sw4[4], bias4[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                sw4[e] = c4 + e < p.N ? __ldg(p.s_w + c4 + e) : 0.f;
+                bias4[e] = c4 + e < p.N && p.bias ? __ldg(p.bias + c4 + e) : 0.f;
+            }
+#pragma unroll 4
+            for (int j = rank + (warp - 2) * S; j < live; j += kEpi * S) {
+                const float st = __ldg(p.s_t + t0 + j);
+                int4 sum = make_int4(0, 0, 0, 0);
+#pragma unroll 4
+                for (int r = 0; r < S; ++r) {
+                    const int4 v = tc::ld_cluster_s32x4(tc::map_rank(mine + j * kRows * 4, r));
+                    sum.x += v.x;
+                    sum.y += v.y;
+                    sum.z += v.z;
+                    sum.w += v.w;
+                }
+                const int s4[4] = {sum.x, sum.y, sum.z, sum.w};
+                float f[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) f[e] = fmaf((float)s4[e] * sw4[e], st, bias4[e]);
+                uint16_t* dst = p.out + (long long)(t0 + j) * p.N + c4;
+                if ((p.N & 3) == 0) {                             // 8-byte aligned, and no lane half inside
+                    if (c4 < p.N) *reinterpret_cast<uint2*>(dst) = make_uint2(pack2(f[0], f[1]), pack2(f[2], f[3]));
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (c4 + e < p.N) dst[e] = float_to_bf16_bits(f[e]);
+                }
+            }
         }
+        tc::cluster_sync();                                       // the others have read this CTA's sums
     }
-    tc::cluster_sync();                                           // the others have read this CTA's sums
     if (warp == 1) tc::tmem_dealloc(tmem, Ly::COLS);
 }
 
 template <int BN>
-cudaError_t launch(const CUtensorMap& mw, const CUtensorMap& mq, MatmulArgs p, int S, cudaStream_t st) {
-    const int smem = Layout<BN>::SMEM + 1024;
-    cudaError_t e = cudaFuncSetAttribute(matmul_few_kernel<BN>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+cudaError_t launch(const CUtensorMap& mw, const CUtensorMap& mq, const MatmulArgs& p, int S, cudaStream_t st) {
+    using Ly = Layout<BN>;
+    const cudaError_t e =
+        cudaFuncSetAttribute(matmul_few_kernel<BN>, cudaFuncAttributeMaxDynamicSharedMemorySize, Ly::smem(Ly::MOST));
     if (e != cudaSuccess) return e;
+    const int nk = (p.K - 1) / kBK + 1, most = (nk - 1) / S + 1;   // a rank's slices
+    const int stages = most < Ly::MOST ? most : Ly::MOST;
     cudaLaunchConfig_t cfg{};
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeClusterDimension;
@@ -369,11 +505,11 @@ cudaError_t launch(const CUtensorMap& mw, const CUtensorMap& mq, MatmulArgs p, i
     at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
     cfg.gridDim = dim3((unsigned)((long long)p.tiles_n * p.tiles_t * S));
     cfg.blockDim = dim3(kWarps * 32);
-    cfg.dynamicSmemBytes = smem;
+    cfg.dynamicSmemBytes = Ly::smem(stages);
     cfg.stream = st;
     cfg.attrs = at;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, matmul_few_kernel<BN>, mw, mq, p, S);
+    cfg.numAttrs = S > 1 ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, matmul_few_kernel<BN>, mw, mq, p, S, stages);
 }
 
 }  // namespace few
@@ -385,22 +521,44 @@ bool operand_map(CUtensorMap* m, const int8_t* base, int rows, int K, int box_ro
                         (unsigned)box_rows, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
+// K split of a call on matmul_few_kernel: the most ranks that leave about a CTA to an SM, or
+// up to 1.75 where each still has 16 slices (two CTAs fit an SM, but clusters beyond what
+// the GPCs hold run after the others: 1536 x 1024 -> 2048 10.4 us with S = 1, 16.0 with 2).
+int split_of(long long tiles, int nk, int sms) {
+    int S = 1;
+    for (int c : {2, 4, 8}) {
+        const long long ctas = tiles * c;
+        if (c > nk || ctas * 4 > 7LL * sms) break;
+        if (ctas * 10 <= (c == 8 ? 10LL : 11LL) * sms || (c < 8 && nk / c >= 16)) S = c;
+    }
+    return S;
+}
+
 }  // namespace
 
+// Which kernel: the first up to 64 tokens, else by an estimate of both, in microseconds.  Few tokens: what a CTA takes
+// besides its K slices, what a second CTA on an SM or a split adds, a slice's bytes through
+// an SM, and half the weights' time from HBM.  Pairs: the same for a 256 x 256 tile's slices
+// (and the unaligned epilogue's stores).  Measured (few, pair):
+//   128 x 2560 -> 10576 12.1, 12.3    192 15.4, 12.5     384 16.8, 18.9     512 27.2, 19.1
+//   256 x 5120 -> 2560  10.8, 17.0    768 16.4, 17.6    1024 21.1, 17.8
+//   192 x 8192 -> 4096  15.8, 24.4    512 21.4, 24.6     768 33.5, 24.9    512^3  6.4, 7.1
 cudaError_t launch_matmul_i8(int T, int K, int N, const int8_t* q, const float* s_t, const int8_t* Wq,
                              const float* s_w, const float* bias, uint16_t* out, int* status, cudaStream_t st) {
     CUtensorMap mw, mq;
     MatmulArgs p{T, K, N, 0, 0, s_t, s_w, bias, out, status};
-    const int sms = device_sm_count(), nk = (K + kBK - 1) / kBK;
+    const int sms = device_sm_count(), nk = tiles_of(K, kBK);
+    const int bn = T <= 16 ? 16 : T <= 32 ? 32 : T <= 64 ? 64 : 128;
+    const long long few_tiles = (long long)tiles_of(N, few::kRows) * tiles_of(T, bn);
     const long long pair_tiles = (long long)tiles_of(T, pair::kTile) * tiles_of(N, pair::kTile);
-    if (T <= 128 || pair_tiles < sms / 4) {
-        const int bn = T <= 16 ? 16 : T <= 32 ? 32 : T <= 64 ? 64 : 128;
+    const int S = split_of(few_tiles, nk, sms);
+    const double load = few_tiles * S > sms ? (double)few_tiles * S / sms : 1.0;
+    const double few_us = 5.2 + 3.0 * (load - 1.0) + (S > 1 ? bn / 160.0 : 0.0) +
+                          load * nk / S * (few::kRows + bn) / 930.0 + 0.5 * (double)N * K / 6.5e6;
+    const double pair_us = 6.5 + (double)((pair_tiles + sms / 2 - 1) / (sms / 2)) * (0.28 * nk + (N % 8 ? 5.0 : 0.0));
+    if (T <= 64 || few_us <= pair_us) {
         p.tiles_n = tiles_of(N, few::kRows);
         p.tiles_t = tiles_of(T, bn);
-        const long long tiles = (long long)p.tiles_n * p.tiles_t;
-        // split K until every SM has a CTA, over at most 8 (the portable cluster) non-empty parts
-        int S = 1;
-        while (S < 8 && tiles * S < sms && 2 * S <= nk) S *= 2;
         if (!operand_map(&mw, Wq, N, K, few::kRows) || !operand_map(&mq, q, T, K, bn)) return cudaErrorInvalidValue;
         if (bn == 16) return few::launch<16>(mw, mq, p, S, st);
         if (bn == 32) return few::launch<32>(mw, mq, p, S, st);
@@ -408,14 +566,14 @@ cudaError_t launch_matmul_i8(int T, int K, int N, const int8_t* q, const float* 
         return few::launch<128>(mw, mq, p, S, st);
     }
     if (!operand_map(&mw, Wq, N, K, pair::kRows) || !operand_map(&mq, q, T, K, pair::kRows)) return cudaErrorInvalidValue;
-    const int smem = pair::SMEM + 1024;
-    const cudaError_t e = cudaFuncSetAttribute(pair::matmul_pair_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess) return e;
     p.tiles_n = tiles_of(N, pair::kTile);
     p.tiles_t = tiles_of(T, pair::kTile);
-    const int pairs = (int)(pair_tiles < sms / 2 ? pair_tiles : sms / 2);
-    pair::matmul_pair_kernel<<<2 * pairs, kWarps * 32, smem, st>>>(mw, mq, p);
-    return cudaGetLastError();
+    if (N % 8 != 0) return pair::launch<true>(mq, mw, mq, p, st);      // the third map is not read
+    CUtensorMap mo;
+    if (!make_tmap_2d(&mo, false, out, (unsigned long long)N, (unsigned long long)T, (unsigned long long)N * 2, 32, 32,
+                      CU_TENSOR_MAP_SWIZZLE_64B))
+        return cudaErrorInvalidValue;
+    return pair::launch<false>(mq, mw, mo, p, st);
 }
 
 }  // namespace ssd
