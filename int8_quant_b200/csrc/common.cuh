@@ -19,6 +19,34 @@ struct Dims {
 // Device status word values (first int32 of the workspace).
 enum : int { kStatusOk = 0, kStatusTimeout = 5 };
 
+// ---------------------------------------------------------------- programmatic launches
+// A kernel launched with launch_programmatic may start while the one ahead of it in the stream
+// still runs: it reads and writes nothing of global memory in front of grid_wait(), which
+// returns once that kernel (and so all ahead of it) is done.  grid_release() lets the next
+// such kernel start.
+__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void grid_release() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+// Launches `kernel` so, in clusters of `cluster` CTAs.
+template <typename... P, typename... A>
+cudaError_t launch_programmatic(void (*kernel)(P...), unsigned grid, int threads, size_t smem, cudaStream_t st,
+                                int cluster, A... args) {
+    cudaLaunchAttribute at[2];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = (unsigned)cluster;
+    at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cfg.attrs = at;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 // ---------------------------------------------------------------- bf16 helpers
 __device__ __forceinline__ float bf16_bits_to_float(uint16_t v) {
     return __uint_as_float(((uint32_t)v) << 16);

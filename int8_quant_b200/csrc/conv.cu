@@ -157,6 +157,8 @@ __device__ __forceinline__ void conv_tile(const ConvArgs& a) {
 template <int W>
 __global__ void __launch_bounds__(kThreads)
 conv_fwd_kernel(const __grid_constant__ ConvArgs a) {
+    grid_release();
+    grid_wait();
     if (blockIdx.x < a.conv_blocks) {
         conv_tile<W>(a);
     } else if (blockIdx.x < a.conv_blocks + a.dt_blocks) {
@@ -194,6 +196,8 @@ conv_fwd_kernel(const __grid_constant__ ConvArgs a) {
 template <int W>
 __global__ void __launch_bounds__(kStepThreads)
 conv_step_kernel(const __grid_constant__ ConvArgs a, uint16_t* state) {
+    grid_release();
+    grid_wait();
     const long long idx = (long long)blockIdx.x * kStepThreads + threadIdx.x;
     if (blockIdx.x < a.conv_blocks) {
         const int nvec = a.C / 8;
@@ -254,10 +258,9 @@ cudaError_t launch_conv_fwd(const ConvDims& d, const ConvIn& in, const ConvOut& 
     a.dt_blocks = a.dt ? blocks_for(blocks_for(rows, kDtRows) * a.H, kThreads) : 0;
     const long long fin = a.fin ? blocks_for((long long)a.B * (d.W - 1) * (a.C / 8), kThreads) : 0;
     const unsigned grid = (unsigned)(a.conv_blocks + a.dt_blocks + fin);
-    if (d.W == 2) conv_fwd_kernel<2><<<grid, kThreads, 0, st>>>(a);
-    else if (d.W == 3) conv_fwd_kernel<3><<<grid, kThreads, 0, st>>>(a);
-    else conv_fwd_kernel<4><<<grid, kThreads, 0, st>>>(a);
-    return cudaGetLastError();
+    if (d.W == 2) return launch_programmatic(conv_fwd_kernel<2>, grid, kThreads, 0, st, 1, a);
+    if (d.W == 3) return launch_programmatic(conv_fwd_kernel<3>, grid, kThreads, 0, st, 1, a);
+    return launch_programmatic(conv_fwd_kernel<4>, grid, kThreads, 0, st, 1, a);
 }
 
 cudaError_t launch_conv_step(const ConvDims& d, const ConvIn& in, uint16_t* state, const ConvOut& out,
@@ -265,10 +268,9 @@ cudaError_t launch_conv_step(const ConvDims& d, const ConvIn& in, uint16_t* stat
     ConvArgs a = conv_args(d, in, out);
     a.conv_blocks = blocks_for((long long)(a.C / 8) * a.B, kStepThreads);
     const unsigned grid = (unsigned)(a.conv_blocks + (a.dt ? blocks_for((long long)a.B * a.H, kStepThreads) : 0));
-    if (d.W == 2) conv_step_kernel<2><<<grid, kStepThreads, 0, st>>>(a, state);
-    else if (d.W == 3) conv_step_kernel<3><<<grid, kStepThreads, 0, st>>>(a, state);
-    else conv_step_kernel<4><<<grid, kStepThreads, 0, st>>>(a, state);
-    return cudaGetLastError();
+    if (d.W == 2) return launch_programmatic(conv_step_kernel<2>, grid, kStepThreads, 0, st, 1, a, state);
+    if (d.W == 3) return launch_programmatic(conv_step_kernel<3>, grid, kStepThreads, 0, st, 1, a, state);
+    return launch_programmatic(conv_step_kernel<4>, grid, kStepThreads, 0, st, 1, a, state);
 }
 
 }  // namespace ssd

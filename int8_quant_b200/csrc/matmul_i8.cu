@@ -97,9 +97,9 @@ __device__ __forceinline__ void store_tokens(const uint32_t (&v)[32], const floa
         if (j < live) dst[j * N] = float_to_bf16_bits(fmaf((float)(int)v[j] * sw, __ldg(s_t + j), bias));
 }
 
-// SWAP: the tile's rows are channels (tm_a: the weights), its columns tokens.
+// SWAP: the tile's rows are channels (tm_a: the weights), its columns tokens.  Clusters of 2.
 template <bool SWAP>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWarps * 32, 1)
+__global__ void __launch_bounds__(kWarps * 32, 1)
 matmul_pair_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
                    const __grid_constant__ CUtensorMap tm_out, const __grid_constant__ MatmulArgs p) {
     extern __shared__ uint8_t smem_raw[];
@@ -123,16 +123,20 @@ matmul_pair_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_consta
         tc::tmem_alloc_pair(tmem_slot, kAcc * kTile);
         tc::tmem_relinquish_pair();
     }
+    if (threadIdx.x == 0) {
+        tc::prefetch_tmap(&tm_a);
+        tc::prefetch_tmap(&tm_b);
+    }
     tc::tc_fence_before();
     __syncthreads();
     tc::cluster_sync();
     tc::tc_fence_after();
     const uint32_t tmem = *tmem_slot;
+    grid_release();
+    grid_wait();
 
     if (warp == 0) {
         if (lane == 0) {
-            tc::prefetch_tmap(&tm_a);
-            tc::prefetch_tmap(&tm_b);
             int s = 0;
             uint32_t phase = 1;                                   // a fresh stage counts as free
             int issued = 0;                                       // stages with a copy issued (up to kStages)
@@ -298,8 +302,8 @@ cudaError_t launch(const CUtensorMap& mq, const CUtensorMap& mw, const CUtensorM
     if (e != cudaSuccess) return e;
     const long long tiles = (long long)p.tiles_t * p.tiles_n;
     const int most = device_sm_count() / 2, pairs = tiles < most ? (int)tiles : most;
-    matmul_pair_kernel<SWAP><<<2 * pairs, kWarps * 32, smem, st>>>(SWAP ? mw : mq, SWAP ? mq : mw, mo, p);
-    return cudaGetLastError();
+    return launch_programmatic(matmul_pair_kernel<SWAP>, 2 * pairs, kWarps * 32, smem, st, 2, SWAP ? mw : mq,
+                               SWAP ? mq : mw, mo, p);
 }
 
 }  // namespace pair
@@ -356,12 +360,17 @@ matmul_few_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constan
         *abort_flag = 0;
         tc::fence_mbar_init();
         tc::fence_proxy_async_smem();
+        tc::prefetch_tmap(&tm_w);
+        tc::prefetch_tmap(&tm_q);
+        grid_wait();
         for (int j = 0; j < first; ++j) load(j, j);
     }
     if (warp == 1) {
         tc::tmem_alloc(tmem_slot, Ly::COLS);
         tc::tmem_relinquish();
     }
+    grid_release();
+    grid_wait();
     tc::tc_fence_before();
     __syncthreads();
     tc::tc_fence_after();
@@ -498,18 +507,8 @@ cudaError_t launch(const CUtensorMap& mw, const CUtensorMap& mq, const MatmulArg
     if (e != cudaSuccess) return e;
     const int nk = (p.K - 1) / kBK + 1, most = (nk - 1) / S + 1;   // a rank's slices
     const int stages = most < Ly::MOST ? most : Ly::MOST;
-    cudaLaunchConfig_t cfg{};
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = S;
-    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-    cfg.gridDim = dim3((unsigned)((long long)p.tiles_n * p.tiles_t * S));
-    cfg.blockDim = dim3(kWarps * 32);
-    cfg.dynamicSmemBytes = Ly::smem(stages);
-    cfg.stream = st;
-    cfg.attrs = at;
-    cfg.numAttrs = S > 1 ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, matmul_few_kernel<BN>, mw, mq, p, S, stages);
+    return launch_programmatic(matmul_few_kernel<BN>, (unsigned)((long long)p.tiles_n * p.tiles_t * S), kWarps * 32,
+                               Ly::smem(stages), st, S, mw, mq, p, S, stages);
 }
 
 }  // namespace few

@@ -84,6 +84,8 @@ rmsnorm_i8_kernel(const __grid_constant__ NormArgs a) {
     const int nv = a.d >> 3, warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nw = blockDim.x >> 5;
     const float inf = __int_as_float(0x7f800000);
     const long long row = blockIdx.x;
+    grid_release();
+    grid_wait();
     RowIn<KIND, VPT> in;
     load_row<KIND, VPT>(a, row, nv, in);
     f32x2 p[VPT][4];
@@ -187,8 +189,7 @@ template <int KIND, int VPT>
 cudaError_t launch_vpt(const NormArgs& a, int T, cudaStream_t st) {
     const int nv = a.d >> 3;
     const int threads = ((nv + VPT - 1) / VPT + 31) / 32 * 32;
-    rmsnorm_i8_kernel<KIND, VPT><<<T, threads, 0, st>>>(a);
-    return cudaGetLastError();
+    return launch_programmatic(rmsnorm_i8_kernel<KIND, VPT>, (unsigned)T, threads, 0, st, 1, a);
 }
 
 // Two vectors a thread up to 320 threads: beyond, CTAs get so large that few fit an SM, and
