@@ -328,9 +328,8 @@ ssd_status ssd_out_proj_status(void* workspace, int tokens, int d_inner, cudaStr
  * that is not finite, or whose sum of squares is not, codes 0 and scale NaN.
  * x : device bf16 [tokens, d]
  * residual, residual_out : device [tokens, d], fp32 if residual_fp32 != 0, else bf16 (then v
- *   is rounded to bf16 before it is normalised).  residual may be null (residual_out is then
- *   bf16: residual_fp32 must be 0); residual_out may be null, and may be `residual` or `x`
- *   itself where the types agree, but must not overlap them otherwise.
+ *   is rounded to bf16 before it is normalised).  Either may be null; residual_out may be
+ *   `residual` or `x` itself where the types agree, but must not overlap them otherwise.
  * weight : device fp32 [d] or null (ones), finite.    eps > 0
  * q : device int8 [tokens, d], written.   scale : device fp32 [tokens], written.
  * values : device bf16 [tokens, d] or null: the values that the codes stand for, q * scale,

@@ -503,7 +503,6 @@ ssd_status ssd_add_rmsnorm_i8(int tokens, int d, const uint16_t* x, const void* 
                               uint16_t* values, cudaStream_t stream) {
     const ssd_status st = norm_dims(tokens, d, eps);
     if (st != SSD_OK) return st;
-    if (!residual && residual_fp32) return SSD_ERR_INVALID_ARG;
     if (tokens == 0) return SSD_OK;
     if (!x || !q || !scale) return SSD_ERR_INVALID_ARG;
     if (!aligned16(x) || !aligned16(residual) || !aligned16(weight) || !aligned16(residual_out) || !aligned16(q) ||

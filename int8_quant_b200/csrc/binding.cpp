@@ -150,7 +150,9 @@ PyObject* add_rmsnorm_i8(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const auto shape = x.sizes();
         const int T = as_int(shape[0], "x"), d = as_int(shape[1], "x");
         const bool res = a[1] != Py_None;
-        const bool fp32 = res && tensor(a[1], "residual").scalar_type() == at::kFloat;
+        // the residual stream's type: the residual's, or without one that of residual_out
+        PyObject* stream_of = res ? a[1] : a[4];
+        const bool fp32 = stream_of != Py_None && tensor(stream_of, "residual").scalar_type() == at::kFloat;
         const at::ScalarType kept = fp32 ? at::kFloat : at::kBFloat16;
         const uint16_t* xp = c.dense<uint16_t>(a[0], "x", at::kBFloat16, shape);
         const void* rp = c.optional<void>(a[1], "residual", kept, shape);

@@ -38,6 +38,7 @@ struct NormArgs {
     const float* w;             // null: ones
     float eps;
     void* res_out;              // may be null, may be in2 or x itself
+    bool res_f32;               // its type
     int8_t* q;
     float* scale;
     uint16_t* values;           // q * scale as bf16, or null
@@ -117,7 +118,7 @@ rmsnorm_i8_kernel(const __grid_constant__ NormArgs a) {
             unpack8(pack8(v), v);
         }
         if (KIND != kGate && a.res_out) {
-            if (KIND == kResF32) {
+            if (KIND == kResF32 || (KIND == kResNone && a.res_f32)) {
                 ulonglong2* op = reinterpret_cast<ulonglong2*>(static_cast<float*>(a.res_out) + row * a.d) + 2 * i;
                 op[0] = make_ulonglong2(v[0], v[1]);
                 op[1] = make_ulonglong2(v[2], v[3]);
@@ -207,7 +208,7 @@ cudaError_t launch_kind(const NormArgs& a, int T, cudaStream_t st) {
 cudaError_t launch_add_rmsnorm_i8(int T, int d, const uint16_t* x, const void* residual, bool fp32, const float* w,
                                   float eps, void* res_out, int8_t* q, float* scale, uint16_t* values,
                                   cudaStream_t st) {
-    const NormArgs a{d, d, x, residual, w, eps, res_out, q, scale, values};
+    const NormArgs a{d, d, x, residual, w, eps, res_out, fp32, q, scale, values};
     if (!residual) return launch_kind<kResNone>(a, T, st);
     return fp32 ? launch_kind<kResF32>(a, T, st) : launch_kind<kResBf16>(a, T, st);
 }
@@ -215,7 +216,7 @@ cudaError_t launch_add_rmsnorm_i8(int T, int d, const uint16_t* x, const void* r
 cudaError_t launch_gated_rmsnorm_i8(int T, int d, const uint16_t* y, const uint16_t* z, long long ld_z,
                                     const float* w, float eps, int8_t* q, float* scale, uint16_t* values,
                                     cudaStream_t st) {
-    return launch_kind<kGate>(NormArgs{d, ld_z, y, z, w, eps, nullptr, q, scale, values}, T, st);
+    return launch_kind<kGate>(NormArgs{d, ld_z, y, z, w, eps, nullptr, false, q, scale, values}, T, st);
 }
 
 }  // namespace ssd

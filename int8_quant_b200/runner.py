@@ -268,3 +268,120 @@ class Decoder:
             return self.y
         ssd.ssd_decode_step_i8(shape, x, dt, self.A, B, C, self.D, self.params, self.state, self.y, stream)
         return self.y
+
+
+class SsdLayer:
+    """One W8A8 Mamba-2 layer: residual norm, in_proj, convolution, scan, gated norm and out_proj, each a call
+    into libssd.so.
+
+    weights, device tensors (d features of the residual stream, E >= 2*H*P + 2*G*N + H rows of in_proj with
+    E % 8 == 0, in the order z | x | B | C | dt, C = H*P + 2*G*N channels):
+      norm [d], gate_norm [H*P] fp32;  in_q [E, d], out_q [d, H*P] int8 with in_s [E], out_s [d] fp32;
+      out_corr [d] fp32 or absent (the mean correction of the output projection);
+      conv_w [width, C], conv_b [C] (or absent), dt_bias [H], A [H], D [H] fp32.
+    dims: (H, P, G, N).  path: the scan's, "bf16" or "w8a8" (then `scales`: the static scales s_B, s_C, s_x, s_s).
+    """
+
+    def __init__(self, weights: dict, dims, path: str, chunk: int = 256, scales: dict | None = None, shift: int = 7,
+                 eps: float = 1e-5):
+        assert path in ("bf16", "w8a8")
+        self.w, self.path, self.chunk, self.eps, self.scales = weights, path, chunk, eps, scales
+        self.H, self.P, self.G, self.N = dims
+        self.hp = self.H * self.P
+        self.ch = self.hp + 2 * self.G * self.N
+        self.E, self.d = weights["in_q"].shape
+        self.width = weights["conv_w"].shape[0]
+        if self.E % 8 or self.E < self.hp + self.ch + self.H:
+            raise ValueError("in_proj's rows: at least 2*H*P + 2*G*N + H of them, and a multiple of 8")
+        self.dev = weights["in_q"].device
+        self.params = None
+        if path == "w8a8":
+            self.params = ssd.i8_params(scales["s_B"], scales["s_C"], scales["s_x"], scales["s_s"], shift)
+        self.status = torch.zeros(1, dtype=torch.int32, device=self.dev)
+
+    def new(self, *shape, dtype=torch.bfloat16):
+        return torch.empty(shape, dtype=dtype, device=self.dev)
+
+    def slices(self, rows):
+        """z, xBC and dt of in_proj's output rows."""
+        hp, ch = self.hp, self.ch
+        return rows[..., :hp], rows[..., hp:hp + ch], rows[..., hp + ch:hp + ch + self.H]
+
+    def zero_state(self, batch: int) -> dict:
+        """The state of `batch` rows ahead of their first token."""
+        t = torch.float32 if self.path == "bf16" else torch.int8
+        return {"conv": torch.zeros((batch, self.width - 1, self.ch), dtype=torch.bfloat16, device=self.dev),
+                "ssd": torch.zeros((batch, self.H, self.P, self.N), dtype=t, device=self.dev)}
+
+    def prefill(self, hidden, residual=None, state: dict | None = None, lengths=None, stream=None):
+        """hidden [b, L, d] bf16; residual [b, L, d] fp32 or bf16, or None (the stream starts here, in fp32); state:
+        what an earlier call returned (None: zeros); lengths [b] int32: the tokens of each row of a padded batch.
+        Returns (the layer's output [b, L, d] bf16, the residual to hand on, the state after each row's last
+        token).  Outputs behind a row's last token mean nothing.  Buffers are torch's, on its current stream:
+        with `stream` given, make that the current one too."""
+        b, L, d = hidden.shape
+        T, w, new = b * L, self.w, self.new
+        q, s = new(T, d, dtype=torch.int8), new(T, dtype=torch.float32)
+        res = None if residual is None else residual.reshape(T, d)
+        res_out = new(T, d, dtype=torch.float32 if res is None else res.dtype)
+        ssd.ssd_add_rmsnorm_i8(hidden.reshape(T, d), res, w["norm"], self.eps, res_out, q, s, stream=stream)
+        rows = new(b, L, self.E)
+        ssd.ssd_matmul_i8(q, s, w["in_q"], w["in_s"], None, rows.view(T, self.E), self.status, stream)
+        _, xbc, dt_raw = self.slices(rows)
+        x, B, C = new(b, L, self.H, self.P), new(b, L, self.G, self.N), new(b, L, self.G, self.N)
+        dt, conv = new(b, L, self.H, dtype=torch.float32), new(b, self.width - 1, self.ch)
+        ssd.ssd_conv_fwd_bf16(xbc, dt_raw, w["conv_w"], w.get("conv_b"), w["dt_bias"], lengths,
+                              None if state is None else state["conv"], x, dt, B, C, conv, stream)
+        y = new(b, L, self.H, self.P)
+        init = None if state is None else state["ssd"]
+        shape = ssd.SsdShape.of(b, L, self.H, self.P, self.G, self.N, self.chunk)
+        ws = new(max(ssd.ssd_workspace_bytes(shape, self.path == "w8a8"), 256), dtype=torch.uint8)
+        if self.path == "bf16":
+            fin = new(b, self.H, self.P, self.N, dtype=torch.float32)
+            ssd.ssd_scan_fwd_bf16_from_state(shape, x, dt, w["A"], B, C, w["D"], init, y, fin, ws, stream)
+        else:
+            fin = new(b, self.H, self.P, self.N, dtype=torch.int8)
+            Bq, Cq = new(*B.shape, dtype=torch.int8), new(*C.shape, dtype=torch.int8)
+            ssd.ssd_quantize_inputs(shape, B, C, self.scales["s_B"], self.scales["s_C"], Bq, Cq, stream)
+            ssd.ssd_scan_fwd_i8_from_state(shape, x, dt, w["A"], Bq, Cq, w["D"], self.params, init, y, fin, ws, stream)
+        qg, out = new(T, self.hp, dtype=torch.int8), new(b, L, d)
+        ssd.ssd_gated_rmsnorm_i8(y.view(T, self.hp), rows.view(T, self.E)[:, :self.hp], w["gate_norm"], self.eps, qg, s,
+                                 stream=stream)
+        ssd.ssd_matmul_i8(qg, s, w["out_q"], w["out_s"], w.get("out_corr"), out.view(T, d), self.status, stream)
+        return out, res_out.view(b, L, d), {"conv": conv, "ssd": fin}
+
+    def decoder(self, state: dict) -> "SsdLayerDecoder":
+        """One-token steps that go on from `state` and update it in place."""
+        return SsdLayerDecoder(self, state)
+
+
+class SsdLayerDecoder:
+    """One-token steps of an SsdLayer on a state, in place.  Each has its own buffers (so do two captured graphs of
+    two decoders), which the next step reuses."""
+
+    def __init__(self, layer: SsdLayer, state: dict):
+        self.layer, self.state = layer, state
+        l, b = layer, state["conv"].shape[0]
+        i8, f32 = torch.int8, torch.float32
+        self.q, self.s, self.rows = l.new(b, l.d, dtype=i8), l.new(b, dtype=f32), l.new(b, l.E)
+        self.x, self.dt = l.new(b, l.H, l.P), l.new(b, l.H, dtype=f32)
+        self.B, self.C = l.new(b, l.G, l.N), l.new(b, l.G, l.N)
+        self.qg, self.out = l.new(b, l.hp, dtype=i8), l.new(b, l.d)
+        self.res = {t: l.new(b, l.d, dtype=t) for t in (torch.float32, torch.bfloat16)}
+        self.z, self.xbc, self.dt_raw = l.slices(self.rows)
+        self.ssd = Decoder(state["ssd"], l.w["A"], l.w["D"], l.path, l.scales,
+                           l.params.decay_shift if l.params is not None else 7)
+
+    def step(self, hidden, residual=None, stream=None):
+        """hidden [b, d] bf16, residual [b, d] fp32 or bf16, or None (the stream starts here, in fp32).  Returns
+        (output [b, d] bf16, the residual to hand on)."""
+        l, w = self.layer, self.layer.w
+        res = self.res[torch.float32 if residual is None else residual.dtype]
+        ssd.ssd_add_rmsnorm_i8(hidden, residual, w["norm"], l.eps, res, self.q, self.s, stream=stream)
+        ssd.ssd_matmul_i8(self.q, self.s, w["in_q"], w["in_s"], None, self.rows, l.status, stream)
+        ssd.ssd_conv_step_bf16(self.xbc, self.dt_raw, w["conv_w"], w.get("conv_b"), w["dt_bias"], self.state["conv"],
+                               self.x, self.dt, self.B, self.C, stream)
+        y = self.ssd.step(self.x, self.dt, self.B, self.C, stream)
+        ssd.ssd_gated_rmsnorm_i8(y.view(-1, l.hp), self.z, w["gate_norm"], l.eps, self.qg, self.s, stream=stream)
+        ssd.ssd_matmul_i8(self.qg, self.s, w["out_q"], w["out_s"], w.get("out_corr"), self.out, l.status, stream)
+        return self.out, res

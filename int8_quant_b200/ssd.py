@@ -307,7 +307,7 @@ def _handle(stream):
 
 def ssd_add_rmsnorm_i8(x, residual, weight, eps: float, residual_out, q, scale, values=None, stream=None):
     """x [T, d] bf16; residual [T, d] fp32 or bf16, or None; weight [d] fp32 or None; residual_out: the residual's
-    type (bf16 without one) or None; q [T, d] int8 and scale [T] fp32 are written, and values [T, d] bf16 (the
+    type (without a residual either) or None; q [T, d] int8 and scale [T] fp32 are written, and values [T, d] bf16 (the
     codes' values, q * scale) unless None."""
     bad = (_BINDING or _binding()).add_rmsnorm_i8(x, residual, weight, eps, residual_out, q, scale, values,
                                                   _handle(stream))

@@ -96,6 +96,10 @@ def test_add_rmsnorm(torch_cuda, T, d, residual, weighted, in_place):
         iq.ssd_add_rmsnorm_i8(x, res, w, 1e-5, None, q2, s2, values)
         assert torch.equal(q, q2) and torch.equal(scale, s2)
         assert torch.equal(values, (q.float() * scale[:, None]).bfloat16())
+    if residual == "none":                 # the start of an fp32 residual stream
+        kept = torch.full((T, d), float("nan"), device="cuda")
+        iq.ssd_add_rmsnorm_i8(x0, None, w, 1e-5, kept, q, scale)
+        assert torch.equal(kept, x0.float())
 
 
 @pytest.mark.parametrize("T,d", NORM_SIZES)

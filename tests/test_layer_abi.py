@@ -15,7 +15,7 @@ def test_add_rmsnorm_refusals():
     f = iq.library().ssd_add_rmsnorm_i8
     good = [4, 64, F, F, 1, F, 1e-5, F, F, F, None, None]
     for i, v, want in [(0, -1, INVALID), (1, 0, INVALID), (1, 40, UNSUPPORTED), (1, 32784, UNSUPPORTED),
-                       (2, None, INVALID), (2, ODD, INVALID), (3, ODD, INVALID), (3, None, INVALID),
+                       (2, None, INVALID), (2, ODD, INVALID), (3, ODD, INVALID),
                        (5, ODD, INVALID), (6, 0.0, INVALID), (6, -1.0, INVALID), (6, float("nan"), INVALID),
                        (7, ODD, INVALID), (8, None, INVALID), (8, ODD, INVALID), (9, None, INVALID), (10, ODD, INVALID)]:
         a = list(good)
