@@ -318,7 +318,9 @@ ssd_status ssd_out_proj_status(void* workspace, int tokens, int d_inner, cudaStr
  *   ssd_add_rmsnorm_i8 -> ssd_matmul_i8 (in_proj; its rows are z | x | B | C | dt) ->
  *   ssd_conv_fwd_bf16 or ssd_conv_step_bf16 -> a scan or a decode step ->
  *   ssd_gated_rmsnorm_i8 -> ssd_matmul_i8 (out_proj)
- * Nothing but the numbers below is kept from one call for the next. */
+ * Outputs must not overlap inputs or each other unless an argument's text allows it.  The
+ * kernels may start while the one ahead of them in the stream ends (programmatic stream
+ * serialisation); they read and write nothing before it has. */
 
 /* Residual addition and RMSNorm of each token, to INT8 codes with one scale per token:
  *   v = x + residual              (fp32; residual null: v = x), kept as residual_out
@@ -357,7 +359,8 @@ ssd_status ssd_gated_rmsnorm_i8(int tokens, int d, const uint16_t* y, const uint
  * status : device int, left alone unless a device-side bounded wait expires, which writes
  *   SSD_ERR_TIMEOUT: clear it once, read it with ssd_workspace_status(status, stream).  Calls
  *   may share it.
- * k % 16 == 0 and k <= 131072, else SSD_ERR_UNSUPPORTED; any tokens >= 0 and n >= 1. */
+ * k % 16 == 0, k <= 131072, 0 <= tokens <= 2^30 and 1 <= n <= 2^30, else
+ * SSD_ERR_UNSUPPORTED (negative: SSD_ERR_INVALID_ARG). */
 ssd_status ssd_matmul_i8(int tokens, int k, int n, const int8_t* q, const float* s_t, const int8_t* Wq,
                          const float* s_w, const float* bias, uint16_t* out, int* status, cudaStream_t stream);
 

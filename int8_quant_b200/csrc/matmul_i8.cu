@@ -362,6 +362,8 @@ matmul_few_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constan
         tc::fence_proxy_async_smem();
         tc::prefetch_tmap(&tm_w);
         tc::prefetch_tmap(&tm_q);
+        // the weights on their way to L2 while the kernel ahead in the stream ends
+        for (int j = 0; j < k1 - k0; ++j) tc::tma_prefetch_2d(&tm_w, (k0 + j) * kBK, n0);
         grid_wait();
         for (int j = 0; j < first; ++j) load(j, j);
     }
