@@ -14,7 +14,7 @@
 // of 8 features a thread, all loads issued before anything else; many small CTAs resident on
 // an SM cover each other's barrier.  Measured, in a graph (6.53 TB/s is the copy bandwidth):
 //   65536 x 2560, fp32 residual   266 us = 6.9 TB/s, with values 318 us = 6.9 TB/s
-//   16384 x 5120, gate             80 us = 5.2 TB/s, with values  96 us = 6.1 TB/s
+//   16384 x 5120, gate             70 us = 6.0 TB/s, with values  90 us = 6.5 TB/s
 // The gate spends two special-function instructions a feature (exponential, reciprocal); with
 // packed fp32 arithmetic it takes half the instructions of the plain form (95 us).  A
 // persistent grid that loads the next token ahead needs twice the registers and was slower:
@@ -77,9 +77,13 @@ __device__ __forceinline__ float warp_max(float v) {
     return __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(v)));
 }
 
-// 64 registers up to four vectors a thread: 1024 threads an SM
+// CTAs of 512 threads that the registers leave room for on an SM: with the gate's arithmetic
+// to hide, 2048 threads of 32 registers are faster (16384 x 5120 70 us, 1024 of 48 76 us); the
+// residual's loads want the registers (135 us with 48, 158 with 32).
+constexpr int resident(int kind, int vpt) { return vpt == 8 ? 1 : vpt == 2 && kind == kGate ? 4 : 2; }
+
 template <int KIND, int VPT>
-__global__ void __launch_bounds__(kMaxThreads, VPT == 8 ? 1 : 2)
+__global__ void __launch_bounds__(kMaxThreads, resident(KIND, VPT))
 rmsnorm_i8_kernel(const __grid_constant__ NormArgs a) {
     __shared__ float2 part[kMaxThreads / 32], row_scale;
     const int nv = a.d >> 3, warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nw = blockDim.x >> 5;
@@ -193,12 +197,12 @@ cudaError_t launch_vpt(const NormArgs& a, int T, cudaStream_t st) {
     return launch_programmatic(rmsnorm_i8_kernel<KIND, VPT>, (unsigned)T, threads, 0, st, 1, a);
 }
 
-// Two vectors a thread up to 320 threads: beyond, CTAs get so large that few fit an SM, and
-// four a thread are faster (16384 tokens with the gate: d = 4096 64 us either way, 5120 80
-// against 81, 8192 168 against 127).
+// Two vectors a thread as long as a few CTAs fit an SM's registers, then four: with a residual
+// up to 320 threads (16384 x 5120 135 us, 139 with four; 8192 216 with four), with the gate up
+// to 512 (16384 x 8192 114 us, 127 with four).
 template <int KIND>
 cudaError_t launch_kind(const NormArgs& a, int T, cudaStream_t st) {
-    if (a.d <= 5120) return launch_vpt<KIND, 2>(a, T, st);
+    if (a.d <= (KIND == kGate ? 8192 : 5120)) return launch_vpt<KIND, 2>(a, T, st);
     if (a.d <= 32 * kMaxThreads) return launch_vpt<KIND, 4>(a, T, st);
     return launch_vpt<KIND, 8>(a, T, st);
 }
