@@ -22,8 +22,9 @@ enum : int { kStatusOk = 0, kStatusTimeout = 5 };
 // ---------------------------------------------------------------- programmatic launches
 // A kernel launched with launch_programmatic may start while the one ahead of it in the stream
 // still runs: it reads and writes nothing of global memory in front of grid_wait(), which
-// returns once that kernel (and so all ahead of it) is done.  grid_release() lets the next
-// such kernel start.
+// returns once that kernel (and so all ahead of it) is done.  What it reads may have been
+// written during its own life, so it uses no read-only loads (__ldg).  grid_release() lets the
+// next such kernel start.
 __device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void grid_release() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
@@ -117,7 +118,7 @@ __device__ __forceinline__ uint4 pack8(const f32x2 (&f)[4]) {
 }
 // 8 consecutive fp32 values (16-byte aligned) as four pairs.
 __device__ __forceinline__ void load8(const float* p, f32x2 (&f)[4]) {
-    const float4 a = __ldg(reinterpret_cast<const float4*>(p)), b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+    const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
     f[0] = pair2(a.x, a.y);
     f[1] = pair2(a.z, a.w);
     f[2] = pair2(b.x, b.y);

@@ -53,7 +53,7 @@ __device__ __forceinline__ float softplus(float v) { return v > 20.f ? v : log1p
 
 __device__ __forceinline__ int row_length(const ConvArgs& a, int b) {
     if (!a.lengths) return a.L;
-    const int n = __ldg(a.lengths + b);
+    const int n = a.lengths[b];
     return n < 0 ? 0 : n > a.L ? a.L : n;
 }
 
@@ -68,7 +68,7 @@ __device__ __forceinline__ uint16_t* out_of(const ConvArgs& a, int c, int* strid
 }
 
 __device__ __forceinline__ void load_params(const float* p, f32x2 (&f)[2]) {
-    const float4 a = __ldg(reinterpret_cast<const float4*>(p));
+    const float4 a = *reinterpret_cast<const float4*>(p);
     f[0] = pair2(a.x, a.y);
     f[1] = pair2(a.z, a.w);
 }
@@ -169,7 +169,7 @@ conv_fwd_kernel(const __grid_constant__ ConvArgs a) {
 #pragma unroll
         for (int j = 0; j < kDtRows; ++j)
             if (row0 + j < rows) raw[j] = a.dt_raw[(row0 + j) * a.ld + h];
-        const float bias = __ldg(a.dt_bias + h);
+        const float bias = a.dt_bias[h];
 #pragma unroll
         for (int j = 0; j < kDtRows; ++j) {
             const long long row = row0 + j;
@@ -231,7 +231,7 @@ conv_step_kernel(const __grid_constant__ ConvArgs a, uint16_t* state) {
         const long long i = idx - a.conv_blocks * kStepThreads;
         if (i >= (long long)a.B * a.H) return;
         const int b = (int)(i / a.H), h = (int)(i % a.H);
-        a.dt[i] = softplus(bf16_bits_to_float(a.dt_raw[b * a.ld + h]) + __ldg(a.dt_bias + h));
+        a.dt[i] = softplus(bf16_bits_to_float(a.dt_raw[b * a.ld + h]) + a.dt_bias[h]);
     }
 }
 

@@ -90,11 +90,11 @@ __device__ __forceinline__ void fill_box(const uint32_t (&v)[32], float st, cons
 
 // 32 columns (tokens) of this thread's channel.  `dst`: the first token's element; `live` of
 // the tokens exist.
-__device__ __forceinline__ void store_tokens(const uint32_t (&v)[32], const float* __restrict__ s_t, float sw,
+__device__ __forceinline__ void store_tokens(const uint32_t (&v)[32], const float* s_t, float sw,
                                              float bias, uint16_t* dst, long long N, int live) {
 #pragma unroll
     for (int j = 0; j < 32; ++j)
-        if (j < live) dst[j * N] = float_to_bf16_bits(fmaf((float)(int)v[j] * sw, __ldg(s_t + j), bias));
+        if (j < live) dst[j * N] = float_to_bf16_bits(fmaf((float)(int)v[j] * sw, s_t[j], bias));
 }
 
 // SWAP: the tile's rows are channels (tm_a: the weights), its columns tokens.  Clusters of 2.
@@ -224,10 +224,10 @@ matmul_pair_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_consta
             const int row = (SWAP ? n0 : t0) + (int)rank * kRows + quarter * 32 + lane;
             const int c = n0 + half + quarter * 32 + lane;
             const bool in = row < (SWAP ? p.N : p.T);
-            srow = in ? __ldg((SWAP ? p.s_w : p.s_t) + row) : 0.f;
-            brow = SWAP && in && p.bias ? __ldg(p.bias + row) : 0.f;
-            ccol = !SWAP && c < p.N ? __ldg(p.s_w + c) : 0.f;
-            bcol = !SWAP && c < p.N && p.bias ? __ldg(p.bias + c) : 0.f;
+            srow = in ? (SWAP ? p.s_w : p.s_t)[row] : 0.f;
+            brow = SWAP && in && p.bias ? p.bias[row] : 0.f;
+            ccol = !SWAP && c < p.N ? p.s_w[c] : 0.f;
+            bcol = !SWAP && c < p.N && p.bias ? p.bias[c] : 0.f;
         };
         load_scales(me);
         for (long long t = me; t < tiles; t += pairs, ++it) {
@@ -426,8 +426,8 @@ matmul_few_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constan
     }
     const int quarter = warp & 3, row = quarter * 32 + lane, ch = n0 + row, part = (warp - 2) / 4;
     const bool in = warp >= 2 && ch < p.N;
-    const float sw = in ? __ldg(p.s_w + ch) : 0.f;
-    const float bias = in && p.bias ? __ldg(p.bias + ch) : 0.f;
+    const float sw = in ? p.s_w[ch] : 0.f;
+    const float bias = in && p.bias ? p.bias[ch] : 0.f;
     const int live = min(BN, p.T - t0);
     int* red = reinterpret_cast<int*>(buf);
     if (warp >= 2) {
@@ -451,7 +451,7 @@ matmul_few_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constan
                     for (int j = 0; j < 16; ++j)
                         if (c + j < live)
                             dst[(long long)(c + j) * p.N] = float_to_bf16_bits(
-                                fmaf((float)(int)v[j] * sw, __ldg(p.s_t + t0 + c + j), bias));
+                                fmaf((float)(int)v[j] * sw, p.s_t[t0 + c + j], bias));
                 }
             }
         }
@@ -467,12 +467,12 @@ matmul_few_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constan
             float sw4[4], bias4[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                sw4[e] = c4 + e < p.N ? __ldg(p.s_w + c4 + e) : 0.f;
-                bias4[e] = c4 + e < p.N && p.bias ? __ldg(p.bias + c4 + e) : 0.f;
+                sw4[e] = c4 + e < p.N ? p.s_w[c4 + e] : 0.f;
+                bias4[e] = c4 + e < p.N && p.bias ? p.bias[c4 + e] : 0.f;
             }
 #pragma unroll 4
             for (int j = rank + (warp - 2) * S; j < live; j += kEpi * S) {
-                const float st = __ldg(p.s_t + t0 + j);
+                const float st = p.s_t[t0 + j];
                 int4 sum = make_int4(0, 0, 0, 0);
 #pragma unroll 4
                 for (int r = 0; r < S; ++r) {
@@ -537,9 +537,9 @@ int split_of(long long tiles, int nk, int sms) {
 
 }  // namespace
 
-// Which kernel: the first up to 64 tokens, else by an estimate of both, in microseconds.  Few tokens: what a CTA takes
-// besides its K slices, what a second CTA on an SM or a split adds, a slice's bytes through
-// an SM, and half the weights' time from HBM.  Pairs: the same for a 256 x 256 tile's slices
+// Which kernel: matmul_few_kernel up to 64 tokens, else by an estimate of both, in
+// microseconds.  Few tokens: what a CTA takes besides its K slices, what a second CTA on an
+// SM or a split adds, a slice's bytes through an SM, and half the weights' time from HBM.  Pairs: the same for a 256 x 256 tile's slices
 // (and the unaligned epilogue's stores).  Measured (few, pair):
 //   128 x 2560 -> 10576 12.1, 12.3    192 15.4, 12.5     384 16.8, 18.9     512 27.2, 19.1
 //   256 x 5120 -> 2560  10.8, 17.0    768 16.4, 17.6    1024 21.1, 17.8

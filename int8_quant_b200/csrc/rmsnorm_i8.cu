@@ -13,8 +13,8 @@
 // the gate, 2 more where the codes' values are asked for.  One CTA per token and VPT vectors
 // of 8 features a thread, all loads issued before anything else; many small CTAs resident on
 // an SM cover each other's barrier.  Measured, in a graph (6.53 TB/s is the copy bandwidth):
-//   65536 x 2560, fp32 residual   266 us = 6.9 TB/s, with values 318 us = 6.9 TB/s
-//   16384 x 5120, gate             70 us = 6.0 TB/s, with values  90 us = 6.5 TB/s
+//   65536 x 2560, fp32 residual   265 us = 7.0 TB/s, with values 318 us = 6.9 TB/s
+//   16384 x 5120, gate             68 us = 6.2 TB/s, with values  89 us = 6.6 TB/s
 // The gate spends two special-function instructions a feature (exponential, reciprocal); with
 // packed fp32 arithmetic it takes half the instructions of the plain form (95 us).  A
 // persistent grid that loads the next token ahead needs twice the registers and was slower:
@@ -77,13 +77,9 @@ __device__ __forceinline__ float warp_max(float v) {
     return __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(v)));
 }
 
-// CTAs of 512 threads that the registers leave room for on an SM: with the gate's arithmetic
-// to hide, 2048 threads of 32 registers are faster (16384 x 5120 70 us, 1024 of 48 76 us); the
-// residual's loads want the registers (135 us with 48, 158 with 32).
-constexpr int resident(int kind, int vpt) { return vpt == 8 ? 1 : vpt == 2 && kind == kGate ? 4 : 2; }
-
-template <int KIND, int VPT>
-__global__ void __launch_bounds__(kMaxThreads, resident(KIND, VPT))
+// RES: CTAs of 512 threads that the registers leave room for on an SM.
+template <int KIND, int VPT, int RES>
+__global__ void __launch_bounds__(kMaxThreads, RES)
 rmsnorm_i8_kernel(const __grid_constant__ NormArgs a) {
     __shared__ float2 part[kMaxThreads / 32], row_scale;
     const int nv = a.d >> 3, warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nw = blockDim.x >> 5;
@@ -93,6 +89,12 @@ rmsnorm_i8_kernel(const __grid_constant__ NormArgs a) {
     grid_wait();
     RowIn<KIND, VPT> in;
     load_row<KIND, VPT>(a, row, nv, in);
+    // With a residual, each vector's weights are loaded ahead of the residual stores in front of
+    // it, which the compiler cannot tell apart from them (2047 x 2048 11.0 -> 9.8 us); four
+    // vectors a thread have no registers for that (16384 x 8192 218 -> 259 us).
+    constexpr bool kEarly = KIND != kGate && VPT == 2;
+    f32x2 w[4] = {both2(1.f), both2(1.f), both2(1.f), both2(1.f)};
+    if (kEarly && a.w && (int)threadIdx.x < nv) load8(a.w + 8 * threadIdx.x, w);
     f32x2 p[VPT][4];
     f32x2 ss2 = both2(0.f);
     float top = 0.f;
@@ -100,7 +102,10 @@ rmsnorm_i8_kernel(const __grid_constant__ NormArgs a) {
     for (int k = 0; k < VPT; ++k) {
         const int i = threadIdx.x + k * blockDim.x;
         if (i >= nv) continue;
-        f32x2 v[4];
+        f32x2 v[4], wk[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) wk[e] = w[e];
+        if (kEarly && k + 1 < VPT && a.w && i + (int)blockDim.x < nv) load8(a.w + 8 * (i + blockDim.x), w);
         unpack8(in.x[k], v);
         if (KIND == kGate) {
             f32x2 z[4];
@@ -130,12 +135,11 @@ rmsnorm_i8_kernel(const __grid_constant__ NormArgs a) {
                 reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.res_out) + row * a.d)[i] = pack8(v);
             }
         }
-        f32x2 w[4] = {both2(1.f), both2(1.f), both2(1.f), both2(1.f)};
-        if (a.w) load8(a.w + 8 * i, w);
+        if (!kEarly && a.w) load8(a.w + 8 * i, wk);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             ss2 = fma2(v[e], v[e], ss2);
-            p[k][e] = mul2(v[e], w[e]);
+            p[k][e] = mul2(v[e], wk[e]);
             const float2 m = split2(p[k][e]);
             top = fmaxf(fmaxf(top, fabsf(m.x)), fabsf(m.y));     // a NaN is dropped here, but not by ss2
         }
@@ -190,21 +194,29 @@ rmsnorm_i8_kernel(const __grid_constant__ NormArgs a) {
     }
 }
 
-template <int KIND, int VPT>
+template <int KIND, int VPT, int RES>
 cudaError_t launch_vpt(const NormArgs& a, int T, cudaStream_t st) {
     const int nv = a.d >> 3;
     const int threads = ((nv + VPT - 1) / VPT + 31) / 32 * 32;
-    return launch_programmatic(rmsnorm_i8_kernel<KIND, VPT>, (unsigned)T, threads, 0, st, 1, a);
+    return launch_programmatic(rmsnorm_i8_kernel<KIND, VPT, RES>, (unsigned)T, threads, 0, st, 1, a);
 }
 
 // Two vectors a thread as long as a few CTAs fit an SM's registers, then four: with a residual
 // up to 320 threads (16384 x 5120 135 us, 139 with four; 8192 216 with four), with the gate up
-// to 512 (16384 x 8192 114 us, 127 with four).
+// to 512 (16384 x 8192 109 us, 127 with four).  The residual's loads want registers (135 us
+// with 48, 158 with 32).  The gate's arithmetic wants warps to hide behind where there are many
+// tokens (16384 x 5120 68 us with 2048 threads of 32 registers an SM, 81 with 1536 of 40); few
+// tokens want their loads at once (128 x 5120 back to back 6.0 and 4.5 us).
 template <int KIND>
 cudaError_t launch_kind(const NormArgs& a, int T, cudaStream_t st) {
-    if (a.d <= (KIND == kGate ? 8192 : 5120)) return launch_vpt<KIND, 2>(a, T, st);
-    if (a.d <= 32 * kMaxThreads) return launch_vpt<KIND, 4>(a, T, st);
-    return launch_vpt<KIND, 8>(a, T, st);
+    if constexpr (KIND == kGate) {
+        if (a.d <= 16 * kMaxThreads)
+            return T <= 2 * device_sm_count() ? launch_vpt<KIND, 2, 3>(a, T, st) : launch_vpt<KIND, 2, 4>(a, T, st);
+    } else {
+        if (a.d <= 5120) return launch_vpt<KIND, 2, 2>(a, T, st);
+    }
+    if (a.d <= 32 * kMaxThreads) return launch_vpt<KIND, 4, 2>(a, T, st);
+    return launch_vpt<KIND, 8, 1>(a, T, st);
 }
 
 }  // namespace
