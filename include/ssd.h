@@ -318,9 +318,11 @@ ssd_status ssd_out_proj_status(void* workspace, int tokens, int d_inner, cudaStr
  *   ssd_add_rmsnorm_i8 -> ssd_matmul_i8 (in_proj; its rows are z | x | B | C | dt) ->
  *   ssd_conv_fwd_bf16 or ssd_conv_step_bf16 -> a scan or a decode step ->
  *   ssd_gated_rmsnorm_i8 -> ssd_matmul_i8 (out_proj)
- * Outputs must not overlap inputs or each other unless an argument's text allows it.  The
- * kernels may start while the one ahead of them in the stream ends (programmatic stream
- * serialisation); they read and write nothing before it has. */
+ * A token's results do not depend on the tokens beside it, on their number or on the call
+ * that forms them (the convolution's two entry points agree bit for bit).  Outputs must not
+ * overlap inputs or each other unless an argument's text allows it.  The kernels may start
+ * while the one ahead of them in the stream ends (programmatic stream serialisation); they
+ * read and write nothing before it has. */
 
 /* Residual addition and RMSNorm of each token, to INT8 codes with one scale per token:
  *   v = x + residual              (fp32; residual null: v = x), kept as residual_out

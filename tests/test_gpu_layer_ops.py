@@ -274,13 +274,15 @@ def _run_conv(c):
                          c["dt"], c["B"], c["C"], c["final"])
 
 
-@pytest.mark.parametrize("b,L", [(1, 1), (2, 2), (3, 3), (1, 31), (2, 32), (2, 33), (1, 130), (5, 257)])
-@pytest.mark.parametrize("dims", [(2, 64, 1, 128), (3, 24, 3, 8), (80, 64, 1, 128)])
-@pytest.mark.parametrize("W,biased,from_state", [(4, True, True), (4, False, False), (3, True, False), (2, True, True)])
+CONV_LENGTHS = [(1, 1), (2, 2), (3, 3), (1, 31), (2, 32), (2, 33), (1, 63), (2, 64), (1, 65), (1, 130), (5, 257)]
+CONV_FORMS = [(4, True, True), (4, False, False), (3, True, False), (2, True, True)]
+CONV_CASES = [(b, L, dims, *form) for b, L in CONV_LENGTHS for dims in [(2, 64, 1, 128), (3, 24, 3, 8)]
+              for form in CONV_FORMS] + [(b, L, (80, 64, 1, 128), 4, True, True) for b, L in [(1, 1), (2, 33), (1, 130)]]
+
+
+@pytest.mark.parametrize("b,L,dims,W,biased,from_state", CONV_CASES)
 def test_conv(torch_cuda, b, L, dims, W, biased, from_state):
     torch = torch_cuda
-    if dims[0] == 80 and (b * L > 140 or W == 3):
-        pytest.skip("the wide shape at its shorter lengths only (time of the oracle)")
     c = _conv_case(torch, L * 11 + W, b, L, *dims, W, biased, from_state)
     _run_conv(c)
     _check_conv(torch, c)
@@ -360,6 +362,79 @@ def test_conv_of_no_tokens_copies_the_state(torch_cuda):
         assert torch.equal(c["final"], c["init"] if from_state else torch.zeros_like(c["final"]))
 
 
+# ---------------------------------------------------------------- long tensors
+
+def test_rows_past_2_to_the_31_elements(torch_cuda):
+    """The last rows of calls whose tensors have more than 2^31 elements, bit for bit those of a call on them alone."""
+    torch = torch_cuda
+    import int8_quant_b200 as iq
+    g = _gen(torch, 5)
+    T, d, last = 530000, 4096, 9                          # 2.17e9 features
+    x = torch.empty(T, d, device="cuda", dtype=torch.bfloat16)
+    tail = _randn(torch, g, last, d, dtype=torch.bfloat16)
+    x.zero_()
+    x[-last:] = tail
+    q, s = torch.empty(T, d, dtype=torch.int8, device="cuda"), torch.empty(T, device="cuda")
+    q2, s2 = torch.empty(last, d, dtype=torch.int8, device="cuda"), torch.empty(last, device="cuda")
+    iq.ssd_add_rmsnorm_i8(x, None, None, 1e-5, None, q, s)
+    iq.ssd_add_rmsnorm_i8(tail, None, None, 1e-5, None, q2, s2)
+    assert torch.equal(q[-last:], q2) and torch.equal(s[-last:], s2) and not q[:-last].any()
+    iq.ssd_gated_rmsnorm_i8(x, x, None, 1e-5, q, s)
+    iq.ssd_gated_rmsnorm_i8(tail, tail, None, 1e-5, q2, s2)
+    assert torch.equal(q[-last:], q2) and torch.equal(s[-last:], s2)
+    del x
+
+    # product: codes and outputs, aligned rows and not
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    small = q2.contiguous()
+    for n in (4100, 4104):
+        W8 = torch.randint(-127, 128, (n, d), generator=g, device="cuda", dtype=torch.int8)
+        sw = torch.rand(n, generator=g, device="cuda")
+        out, out2 = torch.empty(T, n, device="cuda", dtype=torch.bfloat16), torch.empty(last, n, device="cuda").bfloat16()
+        iq.ssd_matmul_i8(q, s, W8, sw, sw, out, st)
+        iq.ssd_matmul_i8(small, s2, W8, sw, sw, out2, st)
+        assert torch.equal(out[-last:], out2)
+        assert torch.equal(out[:1], sw.bfloat16()[None])   # a token of zeros: the bias
+        del out
+    assert iq.ssd_workspace_status(st) == 0
+    del q, s
+
+    # convolution: two rows of a batch, the second beyond 2^31 elements
+    c = _conv_case(torch, 3, 1, 70, 4, 64, 1, 128, 4)
+    ch, L, ld = c["xbc"].shape[2], 1100000, 1024
+    rows = torch.zeros(2, L, ld, device="cuda", dtype=torch.bfloat16)
+    rows[1, -70:, :ch] = c["xbc"][0]
+    rows[1, -70:, ch:ch + 4] = c["dt_raw"][0]
+    big = {"x": (2, L, 4, 64), "B": (2, L, 1, 128), "C": (2, L, 1, 128)}
+    big = {k: torch.empty(v, device="cuda", dtype=torch.bfloat16) for k, v in big.items()}
+    dt, fin = torch.empty(2, L, 4, device="cuda"), torch.empty(2, 3, ch, device="cuda", dtype=torch.bfloat16)
+    iq.ssd_conv_fwd_bf16(rows[:, :, :ch], rows[:, :, ch:ch + 4], c["weight"], c["bias"], c["dt_bias"], None, None,
+                         big["x"], dt, big["B"], big["C"], fin)
+    _run_conv(c)                                           # from zeros, as the long row's inputs ahead of it are
+    for k in big:
+        assert torch.equal(big[k][1, -70:], c[k][0]), k
+    assert torch.equal(dt[1, -70:], c["dt"][0]) and torch.equal(fin[1], c["final"][0])
+
+
+@pytest.mark.parametrize("N", [2048, 2050])
+def test_product_of_a_token_does_not_depend_on_its_batch(torch_cuda, N):
+    """Few tokens or many, K split or not: the same bits (exact sums, one way of scaling)."""
+    torch = torch_cuda
+    import int8_quant_b200 as iq
+    g = _gen(torch, N)
+    T, K = 1500, 1024
+    q = torch.randint(-127, 128, (T, K), generator=g, device="cuda", dtype=torch.int8)
+    W8 = torch.randint(-127, 128, (N, K), generator=g, device="cuda", dtype=torch.int8)
+    s, sw, b = torch.rand(T, generator=g, device="cuda"), torch.rand(N, generator=g, device="cuda"), _randn(torch, g, N)
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out = torch.empty(T, N, device="cuda").bfloat16()
+    iq.ssd_matmul_i8(q, s, W8, sw, b, out, st)
+    for n in (1, 16, 24, 60, 120, 400):
+        part = torch.empty(n, N, device="cuda").bfloat16()
+        iq.ssd_matmul_i8(q[:n], s[:n], W8, sw, b, part, st)
+        assert torch.equal(part, out[:n]), n
+
+
 # ---------------------------------------------------------------- refusals of the binding
 
 def test_binding_refuses_wrong_tensors(torch_cuda):
@@ -404,6 +479,38 @@ def test_binding_refuses_wrong_tensors(torch_cuda):
 
 
 # ---------------------------------------------------------------- streams and graphs
+
+def test_from_four_threads_at_a_time(torch_cuda):
+    """Four host threads, each with a stream and buffers of its own: the bits of one."""
+    import threading
+    torch = torch_cuda
+    import int8_quant_b200 as iq
+    g = _gen(torch, 1)
+    x, z = _randn(torch, g, 40, 1024, dtype=torch.bfloat16), _randn(torch, g, 40, 1024, dtype=torch.bfloat16)
+    W8 = torch.randint(-127, 128, (1500, 1024), generator=g, device="cuda", dtype=torch.int8)
+    sw, status = torch.rand(1500, generator=g, device="cuda"), torch.zeros(1, dtype=torch.int32, device="cuda")
+    results = {}
+
+    def work(name, reps):
+        stream = torch.cuda.Stream()
+        with torch.cuda.stream(stream):
+            q, s = torch.empty(40, 1024, dtype=torch.int8, device="cuda"), torch.empty(40, device="cuda")
+            out = torch.empty(40, 1500, device="cuda").bfloat16()
+            for _ in range(reps):
+                iq.ssd_gated_rmsnorm_i8(x, z, None, 1e-5, q, s)
+                iq.ssd_matmul_i8(q, s, W8, sw, None, out, status)
+        stream.synchronize()
+        results[name] = out
+
+    work("ref", 1)
+    threads = [threading.Thread(target=work, args=(i, 100)) for i in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert all(torch.equal(results[i], results["ref"]) for i in range(4))
+    assert iq.ssd_workspace_status(status) == 0
+
 
 def test_on_a_side_stream_and_in_two_graphs(torch_cuda):
     """Each operator on a stream of its own, then captured in two graphs that share every buffer but the outputs and
