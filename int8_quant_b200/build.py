@@ -53,7 +53,7 @@ def build_binding(verbose: bool = False) -> str:
     inc = [os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
            sysconfig.get_paths()["include"]]
     # nvcc hands a .cpp to its host compiler: the library's own toolchain and C++ runtime
-    cmd = [_nvcc(), "-O2", "-std=c++17", "-Xcompiler", "-fPIC", "-shared",
+    cmd = [_nvcc(), "-Wno-deprecated-gpu-targets", "-O2", "-std=c++17", "-Xcompiler", "-fPIC", "-shared",
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
            *[f for i in inc for f in ("-isystem", i)], "-o", BINDING + ".tmp", os.path.join(CSRC, "binding.cpp"),
            "-L" + HERE, "-l:libssd.so", "-Xlinker", "-rpath", "-Xlinker", "$ORIGIN",

@@ -10,18 +10,18 @@
 #include <ATen/core/Tensor.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
+#include <c10/util/SmallVector.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <optional>
 #include <stdexcept>
 #include <string>
-#include <vector>
 
 #include "../../include/ssd.h"
 
 namespace {
 
-using Sizes = std::vector<int64_t>;
+using Sizes = c10::SmallVector<int64_t, 5>;                        // on the stack
 
 // A refusal: status SSD_ERR_INVALID_ARG with its reason.
 struct Refused : std::runtime_error {
@@ -239,7 +239,7 @@ struct Conv {
         Sizes s(xt.sizes().begin(), xt.sizes().begin() + lead_n);
         const auto with = [&](std::initializer_list<int64_t> tail) {
             Sizes v = s;
-            v.insert(v.end(), tail);
+            v.append(tail.begin(), tail.end());
             return v;
         };
         xbc = c.rows(xbc_o, "xbc", with({ch}), &ld);
