@@ -45,7 +45,9 @@ cudaError_t launch_programmatic(void (*kernel)(P...), unsigned grid, int threads
     cfg.stream = st;
     cfg.attrs = at;
     cfg.numAttrs = cluster > 1 ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, kernel, args...);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
+    if (e != cudaSuccess) cudaGetLastError();           // reported here, not to the next one who asks
+    return e;
 }
 
 // ---------------------------------------------------------------- bf16 helpers

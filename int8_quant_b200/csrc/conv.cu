@@ -14,15 +14,16 @@
 // (3 CTAs an SM) 251 and 274; plain instead of packed fp32 arithmetic 258 and 283; a window
 // slid along registers, without the staging, 344.  Blocks behind those of the convolution form
 // dt and the final state.
-// conv_step_kernel: one token; a thread owns 8 channels of a batch row and shifts their
-// state in place.
+// conv_step_kernel: one token; a thread owns 8 channels of one or two batch rows and shifts
+// their state in place (8 x 5376 channels in a graph 1.7 us, the launch; 128 x 10240, 21 MB,
+// 3.7 us = 5.7 TB/s from L2).
 #include "kernels.h"
 
 namespace ssd {
 
 namespace {
 
-constexpr int kStepThreads = 256;
+constexpr int kStepThreads = 128;
 constexpr int kThreads = 128;               // of conv_fwd_kernel
 constexpr int kTile = 64;                   // its tokens
 constexpr int kBlock = 256;                 // its channels
@@ -193,40 +194,54 @@ conv_fwd_kernel(const __grid_constant__ ConvArgs a) {
     }
 }
 
-template <int W>
+// R batch rows a thread: their parameters are read once.
+template <int W, int R>
 __global__ void __launch_bounds__(kStepThreads)
 conv_step_kernel(const __grid_constant__ ConvArgs a, uint16_t* state) {
     grid_release();
     grid_wait();
     const long long idx = (long long)blockIdx.x * kStepThreads + threadIdx.x;
     if (blockIdx.x < a.conv_blocks) {
-        const int nvec = a.C / 8;
+        const int nvec = a.C / 8, sv = nvec;
         const int c = (int)(idx % nvec) * 8;
-        const int b = (int)(idx / nvec);
+        const long long b = idx / nvec * R;
         if (b >= a.B) return;
-        uint4 s[W];
-        uint4* sp = reinterpret_cast<uint4*>(state + (long long)b * (W - 1) * a.C + c);
-        const int sv = a.C / 8;
+        const int rows = min(R, (int)(a.B - b));
+        // every load is ahead of the first store, which the compiler cannot tell apart from them
+        uint4 s[R][W];
+        uint4* sp = reinterpret_cast<uint4*>(state + b * (W - 1) * a.C + c);
 #pragma unroll
-        for (int i = 0; i + 1 < W; ++i) s[i] = sp[(long long)i * sv];
-        s[W - 1] = *reinterpret_cast<const uint4*>(a.xbc + b * a.ld + c);
-        f32x2 u[4] = {0, 0, 0, 0};
-        if (a.bias) load8(a.bias + c, u);
+        for (int r = 0; r < R; ++r) {
+            if (r >= rows) break;
 #pragma unroll
-        for (int i = 0; i < W; ++i) {
-            f32x2 w[4], h[4];
-            load8(a.w + (long long)i * a.C + c, w);
-            unpack8(s[i], h);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) u[e] = fma2(w[e], h[e], u[e]);
-            if (i > 0) sp[(long long)(i - 1) * sv] = s[i];
+            for (int i = 0; i + 1 < W; ++i) s[r][i] = sp[(long long)(r * (W - 1) + i) * sv];
+            s[r][W - 1] = *reinterpret_cast<const uint4*>(a.xbc + (b + r) * a.ld + c);
         }
+        f32x2 w[W][4], bias[4] = {0, 0, 0, 0};
+        if (a.bias) load8(a.bias + c, bias);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) u[e] = fast_silu2(u[e]);
+        for (int i = 0; i < W; ++i) load8(a.w + (long long)i * a.C + c, w[i]);
         int stride;
         uint16_t* out = out_of(a, c, &stride);
-        out += (long long)b * stride;
-        *reinterpret_cast<uint4*>(out) = pack8(u);
+        out += b * stride;
+#pragma unroll
+        for (int r = 0; r < R; ++r, out += stride) {
+            if (r >= rows) break;
+            f32x2 u[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) u[e] = bias[e];
+#pragma unroll
+            for (int i = 0; i < W; ++i) {
+                f32x2 h[4];
+                unpack8(s[r][i], h);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) u[e] = fma2(w[i][e], h[e], u[e]);
+                if (i > 0) sp[(long long)(r * (W - 1) + i - 1) * sv] = s[r][i];
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) u[e] = fast_silu2(u[e]);
+            *reinterpret_cast<uint4*>(out) = pack8(u);
+        }
     } else {
         const long long i = idx - a.conv_blocks * kStepThreads;
         if (i >= (long long)a.B * a.H) return;
@@ -263,14 +278,22 @@ cudaError_t launch_conv_fwd(const ConvDims& d, const ConvIn& in, const ConvOut& 
     return launch_programmatic(conv_fwd_kernel<4>, grid, kThreads, 0, st, 1, a);
 }
 
+template <int R>
+static cudaError_t launch_step(const ConvDims& d, ConvArgs a, uint16_t* state, cudaStream_t st) {
+    a.conv_blocks = blocks_for((long long)(a.C / 8) * (((long long)a.B + R - 1) / R), kStepThreads);
+    const unsigned grid = (unsigned)(a.conv_blocks + (a.dt ? blocks_for((long long)a.B * a.H, kStepThreads) : 0));
+    if (d.W == 2) return launch_programmatic(conv_step_kernel<2, R>, grid, kStepThreads, 0, st, 1, a, state);
+    if (d.W == 3) return launch_programmatic(conv_step_kernel<3, R>, grid, kStepThreads, 0, st, 1, a, state);
+    return launch_programmatic(conv_step_kernel<4, R>, grid, kStepThreads, 0, st, 1, a, state);
+}
+
+// Two rows a thread where one each would be more threads than the GPU holds at a time (128 x
+// 5376 channels 3.3 us with one, 3.4 with two; 128 x 10240 4.2, 3.7; 256 x 10240 7.1, 6.1).
 cudaError_t launch_conv_step(const ConvDims& d, const ConvIn& in, uint16_t* state, const ConvOut& out,
                              cudaStream_t st) {
-    ConvArgs a = conv_args(d, in, out);
-    a.conv_blocks = blocks_for((long long)(a.C / 8) * a.B, kStepThreads);
-    const unsigned grid = (unsigned)(a.conv_blocks + (a.dt ? blocks_for((long long)a.B * a.H, kStepThreads) : 0));
-    if (d.W == 2) return launch_programmatic(conv_step_kernel<2>, grid, kStepThreads, 0, st, 1, a, state);
-    if (d.W == 3) return launch_programmatic(conv_step_kernel<3>, grid, kStepThreads, 0, st, 1, a, state);
-    return launch_programmatic(conv_step_kernel<4>, grid, kStepThreads, 0, st, 1, a, state);
+    const ConvArgs a = conv_args(d, in, out);
+    return (long long)(a.C / 8) * a.B > 768LL * device_sm_count() ? launch_step<2>(d, a, state, st)
+                                                                   : launch_step<1>(d, a, state, st);
 }
 
 }  // namespace ssd

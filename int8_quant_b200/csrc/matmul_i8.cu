@@ -89,12 +89,16 @@ __device__ __forceinline__ void fill_box(const uint32_t (&v)[32], float st, cons
 }
 
 // 32 columns (tokens) of this thread's channel.  `dst`: the first token's element; `live` of
-// the tokens exist.
-__device__ __forceinline__ void store_tokens(const uint32_t (&v)[32], const float* s_t, float sw,
-                                             float bias, uint16_t* dst, long long N, int live) {
+// the tokens exist; `in`: the channel does.  Lane j loads token j's scale ahead of the stores,
+// which the compiler cannot tell apart from it.
+__device__ __forceinline__ void store_tokens(const uint32_t (&v)[32], const float* s_t, float sw, float bias,
+                                             uint16_t* dst, long long N, int live, int lane, bool in) {
+    const float scale = lane < live ? s_t[lane] : 0.f;
 #pragma unroll
-    for (int j = 0; j < 32; ++j)
-        if (j < live) dst[j * N] = float_to_bf16_bits(fmaf((float)(int)v[j] * sw, s_t[j], bias));
+    for (int j = 0; j < 32; ++j) {
+        const float st = __shfl_sync(0xffffffffu, scale, j);
+        if (in && j < live) dst[j * N] = float_to_bf16_bits(fmaf((float)(int)v[j] * sw, st, bias));
+    }
 }
 
 // SWAP: the tile's rows are channels (tm_a: the weights), its columns tokens.  Clusters of 2.
@@ -261,12 +265,11 @@ matmul_pair_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_consta
             if (lane == 0) tc::mbar_arrive_cluster(tc::map_rank(tc::smem_u32(bar + B_AEMPTY + a), 0));
             if (SWAP) {
                 const int row = row0 + lane;
-                if (row < p.N) {
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int c = t0 + half + i * 32;
-                        store_tokens(v[i], p.s_t + c, st, sb, p.out + (long long)c * p.N + row, p.N, p.T - c);
-                    }
+                for (int i = 0; i < 4; ++i) {
+                    const int c = t0 + half + i * 32;
+                    store_tokens(v[i], p.s_t + c, st, sb, p.out + (long long)c * p.N + row, p.N, p.T - c, lane,
+                                 row < p.N);
                 }
             } else if (row0 < p.T && n0 + half < p.N) {
 #pragma unroll
@@ -446,12 +449,16 @@ matmul_few_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constan
                 if (S > 1) {
 #pragma unroll
                     for (int j = 0; j < 16; ++j) red[(c + j) * kRows + row] = (int)v[j];
-                } else if (in) {
+                } else {
+                    const int mine = c + (lane & 15);             // this lane's token, for its scale
+                    const float scale = mine < live ? p.s_t[t0 + mine] : 0.f;
 #pragma unroll
-                    for (int j = 0; j < 16; ++j)
-                        if (c + j < live)
-                            dst[(long long)(c + j) * p.N] = float_to_bf16_bits(
-                                fmaf((float)(int)v[j] * sw, p.s_t[t0 + c + j], bias));
+                    for (int j = 0; j < 16; ++j) {
+                        const float st = __shfl_sync(0xffffffffu, scale, j);
+                        if (in && c + j < live)
+                            dst[(long long)(c + j) * p.N] =
+                                float_to_bf16_bits(fmaf((float)(int)v[j] * sw, st, bias));
+                    }
                 }
             }
         }
@@ -470,9 +477,12 @@ matmul_few_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constan
                 sw4[e] = c4 + e < p.N ? p.s_w[c4 + e] : 0.f;
                 bias4[e] = c4 + e < p.N && p.bias ? p.bias[c4 + e] : 0.f;
             }
+            // lane i loads the scale of the warp's i-th token (at most BN / kEpi of them)
+            const int j0 = rank + (warp - 2) * S, mine_j = j0 + lane * kEpi * S;
+            const float scale = mine_j < live ? p.s_t[t0 + mine_j] : 0.f;
 #pragma unroll 4
-            for (int j = rank + (warp - 2) * S; j < live; j += kEpi * S) {
-                const float st = p.s_t[t0 + j];
+            for (int j = j0, i = 0; j < live; j += kEpi * S, ++i) {
+                const float st = __shfl_sync(0xffffffffu, scale, i);
                 int4 sum = make_int4(0, 0, 0, 0);
 #pragma unroll 4
                 for (int r = 0; r < S; ++r) {
