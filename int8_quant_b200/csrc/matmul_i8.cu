@@ -6,10 +6,10 @@
 //
 //   matmul_pair_kernel  many tokens: a CTA pair (cta_group::2) per 256 x 256 output tile,
 //                       persistent, a ring of K slices, two accumulators.  Its rows (TMEM
-//                       lanes) are tokens and its columns channels where n % 8 == 0: tiles
-//                       leave through shared memory by TMA.  Otherwise no row of the output
-//                       is aligned, and the rows are channels: a warp stores 32 channels
-//                       of a token at a time, 64 contiguous bytes whatever their alignment.
+//                       lanes) are tokens and its columns channels.  Tiles leave through
+//                       shared memory, by TMA where n % 8 == 0; otherwise no row of the output
+//                       is aligned, and each is stored from a copy that is shifted in shared
+//                       memory until their 16-byte vectors match.
 //   matmul_few_kernel   few tokens or few tiles: one 128-channel tile (rows) of up to 128
 //                       tokens per cluster, the K axis split over the cluster's CTAs and
 //                       the INT32 partial sums joined through distributed shared memory.
@@ -44,15 +44,23 @@ namespace pair {
 
 constexpr int kRows = 128;                            // rows of each operand per CTA; the pair's tile is 256 x 256
 constexpr int kTile = 2 * kRows;
-constexpr int kStages = 6, kAcc = 2;
+constexpr int kAcc = 2;
 constexpr int kOpBytes = kRows * kBK;
-constexpr int kOutBytes = 32 * 64;                   // a warp's 32 rows of 32 bf16 columns, on their way out
-constexpr int OFF_A = 0, OFF_B = kStages * kOpBytes, OFF_OUT = 2 * kStages * kOpBytes;
-constexpr int OFF_COL = OFF_OUT + kEpi * kOutBytes;   // [kAcc][2][kTile] fp32: the columns' scales and biases
-constexpr int OFF_BAR = OFF_COL + kAcc * 2 * kTile * 4;
-constexpr int B_FULL = 0, B_EMPTY = kStages, B_AFULL = 2 * kStages, B_AEMPTY = B_AFULL + kAcc,
-              B_DRAIN = B_AEMPTY + kAcc, NBAR = B_DRAIN + 1;
-constexpr int OFF_FLAG = OFF_BAR + NBAR * 8, OFF_TMEM = OFF_FLAG + 8, SMEM = OFF_TMEM + 8;
+
+// ALIGNED: n % 8 == 0, stores by TMA.
+template <bool ALIGNED>
+struct Layout {
+    static constexpr int STAGES = ALIGNED ? 6 : 5;
+    // a warp's 32 rows on their way out: 32 bf16 columns, or 64 and room to shift them by up to 7
+    static constexpr int OUT_ROW = ALIGNED ? 64 : 144, OUT = 32 * OUT_ROW;
+    static constexpr int OFF_A = 0, OFF_B = STAGES * kOpBytes, OFF_OUT = 2 * STAGES * kOpBytes;
+    static constexpr int OFF_COL = OFF_OUT + kEpi * OUT;  // [kAcc][2][kTile] fp32: the columns' scales and biases
+    static constexpr int OFF_BAR = OFF_COL + kAcc * 2 * kTile * 4;
+    static constexpr int B_FULL = 0, B_EMPTY = STAGES, B_AFULL = 2 * STAGES, B_AEMPTY = B_AFULL + kAcc,
+                         B_DRAIN = B_AEMPTY + kAcc, NBAR = B_DRAIN + 1;
+    static constexpr int OFF_FLAG = OFF_BAR + NBAR * 8, OFF_TMEM = OFF_FLAG + 8, SMEM = OFF_TMEM + 8;
+    static_assert(SMEM + 1024 <= 227 * 1024, "shared memory of a CTA");
+};
 constexpr int kGroup = 8;                             // token tiles that share the weights while they are in L2
 
 // Tile `t` of the persistent order: groups of kGroup token tiles, in a group all channel
@@ -88,29 +96,71 @@ __device__ __forceinline__ void fill_box(const uint32_t (&v)[32], float st, cons
     }
 }
 
-// 32 columns (tokens) of this thread's channel.  `dst`: the first token's element; `live` of
-// the tokens exist; `in`: the channel does.  Lane j loads token j's scale ahead of the stores,
-// which the compiler cannot tell apart from it.
-__device__ __forceinline__ void store_tokens(const uint32_t (&v)[32], const float* s_t, float sw, float bias,
-                                             uint16_t* dst, long long N, int live, int lane, bool in) {
-    const float scale = lane < live ? s_t[lane] : 0.f;
+// 64 columns of a warp's 32 rows to rows of `n` elements of no alignment: `dst` points at this
+// lane's row, column 0 of the 64; `rows` and `cols` of them exist.  Each row is written to
+// shared memory shifted by the elements that its first lacks to a 16-byte boundary, so that
+// the row's aligned vectors are vectors there; then 8 lanes store a row's, and its up to 7
+// elements in front of and behind them one by one.  4096 x 1024 -> 8193 takes 51 us (8208,
+// aligned, 34); 32 two-byte stores a row, from a tile with the channels in its rows, took 66.
+__device__ __forceinline__ void store_shifted(const uint32_t (&lo)[32], const uint32_t (&hi)[32], float st,
+                                              const float* sw, const float* bias, uint8_t* buf, int lane,
+                                              uint16_t* dst, int rows, int cols) {
+    constexpr int kPitch = Layout<false>::OUT_ROW;
+    const int sh = (int)(((uintptr_t)dst >> 1) & 7);              // elements past the boundary
+    const bool odd = sh & 1;
+    uint32_t* mine = reinterpret_cast<uint32_t*>(buf + lane * kPitch) + (sh >> 1);
+    __syncwarp();                                                 // the rows before have been read
+    float before = 0.f;                                           // column 4 j - 1
 #pragma unroll
-    for (int j = 0; j < 32; ++j) {
-        const float st = __shfl_sync(0xffffffffu, scale, j);
-        if (in && j < live) dst[j * N] = float_to_bf16_bits(fmaf((float)(int)v[j] * sw, st, bias));
+    for (int j = 0; j < 16; ++j) {
+        const float4 w = *reinterpret_cast<const float4*>(sw + 4 * j), b = *reinterpret_cast<const float4*>(bias + 4 * j);
+        const auto acc = [&](int e) { return (float)(int)(j < 8 ? lo[(4 * j + e) & 31] : hi[(4 * j + e) & 31]); };
+        const f32x2 st2 = both2(st);
+        const float2 x = split2(fma2(mul2(pair2(acc(0), acc(1)), pair2(w.x, w.y)), st2, pair2(b.x, b.y)));
+        const float2 y = split2(fma2(mul2(pair2(acc(2), acc(3)), pair2(w.z, w.w)), st2, pair2(b.z, b.w)));
+        mine[2 * j] = odd ? pack2(before, x.x) : pack2(x.x, x.y);
+        mine[2 * j + 1] = odd ? pack2(x.y, y.x) : pack2(y.x, y.y);
+        before = y.y;
+    }
+    if (odd) mine[32] = pack2(before, 0.f);
+    __syncwarp();
+    const int l8 = lane & 7;
+#pragma unroll 4
+    for (int r0 = 0; r0 < 32; r0 += 4) {
+        const int r = r0 + (lane >> 3);                           // 32 rows have addresses, whether they exist or not
+        uint16_t* d = reinterpret_cast<uint16_t*>(
+            __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(dst), r));
+        const int s = (int)(((uintptr_t)d >> 1) & 7), head = min((8 - s) & 7, cols);
+        const int nv = (cols - head) >> 3, tail = cols - head - 8 * nv;
+        const uint16_t* row = reinterpret_cast<const uint16_t*>(buf + r * kPitch) + s;
+        if (r < rows && l8 < nv) {
+            const int e = head + 8 * l8;
+            *reinterpret_cast<uint4*>(d + e) = *reinterpret_cast<const uint4*>(row + e);
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int i = l8 + 8 * h;
+            if (r < rows && i < head + tail) {
+                const int e = i < head ? i : cols - tail + (i - head);
+                d[e] = row[e];
+            }
+        }
     }
 }
 
-// SWAP: the tile's rows are channels (tm_a: the weights), its columns tokens.  Clusters of 2.
-template <bool SWAP>
+// Clusters of 2.
+template <bool ALIGNED>
 __global__ void __launch_bounds__(kWarps * 32, 1)
-matmul_pair_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
+matmul_pair_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_w,
                    const __grid_constant__ CUtensorMap tm_out, const __grid_constant__ MatmulArgs p) {
+    using Ly = Layout<ALIGNED>;
+    constexpr int kStages = Ly::STAGES, B_FULL = Ly::B_FULL, B_EMPTY = Ly::B_EMPTY, B_AFULL = Ly::B_AFULL,
+                  B_AEMPTY = Ly::B_AEMPTY, B_DRAIN = Ly::B_DRAIN;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* sm = smem_raw + ((1024u - (tc::smem_u32(smem_raw) & 1023u)) & 1023u);
-    uint64_t* bar = reinterpret_cast<uint64_t*>(sm + OFF_BAR);
-    volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + OFF_FLAG);
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + OFF_TMEM);
+    uint64_t* bar = reinterpret_cast<uint64_t*>(sm + Ly::OFF_BAR);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + Ly::OFF_FLAG);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + Ly::OFF_TMEM);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = tc::cluster_rank();
     const bool leader = rank == 0;
@@ -119,7 +169,7 @@ matmul_pair_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_consta
     const int pairs = gridDim.x >> 1, me = blockIdx.x >> 1;
     if (threadIdx.x == 0) {
         // an accumulator is free once the epilogue warps of both CTAs have read it
-        for (int i = 0; i < NBAR; ++i) tc::mbar_init(bar + i, i >= B_AEMPTY && i < B_DRAIN ? 2 * kEpi : 1);
+        for (int i = 0; i < Ly::NBAR; ++i) tc::mbar_init(bar + i, i >= B_AEMPTY && i < B_DRAIN ? 2 * kEpi : 1);
         *abort_flag = 0;
         tc::fence_mbar_init();
     }
@@ -128,8 +178,8 @@ matmul_pair_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_consta
         tc::tmem_relinquish_pair();
     }
     if (threadIdx.x == 0) {
-        tc::prefetch_tmap(&tm_a);
-        tc::prefetch_tmap(&tm_b);
+        tc::prefetch_tmap(&tm_q);
+        tc::prefetch_tmap(&tm_w);
     }
     tc::tc_fence_before();
     __syncthreads();
@@ -148,14 +198,15 @@ matmul_pair_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_consta
             for (long long t = me; ok && t < tiles; t += pairs) {
                 int n0, t0;
                 tile_at(p, t, &n0, &t0);
-                const int a0 = (SWAP ? n0 : t0) + (int)rank * kRows, b0 = (SWAP ? t0 : n0) + (int)rank * kRows;
+                n0 += (int)rank * kRows;
+                t0 += (int)rank * kRows;
                 for (int k = 0; k < nk; ++k) {
                     if (!(ok = tc::wait_or_abort(bar + B_EMPTY + s, phase, abort_flag, p.status, kStatusTimeout))) break;
                     // both CTAs' loads of a stage count on the even CTA's barrier
                     if (leader) tc::mbar_arrive_expect_tx(bar + B_FULL + s, 4 * kOpBytes);
                     const uint32_t full = tc::map_rank(tc::smem_u32(bar + B_FULL + s), 0);
-                    tc::tma_load_2d_pair(sm + OFF_A + s * kOpBytes, &tm_a, full, k * kBK, a0);
-                    tc::tma_load_2d_pair(sm + OFF_B + s * kOpBytes, &tm_b, full, k * kBK, b0);
+                    tc::tma_load_2d_pair(sm + Ly::OFF_A + s * kOpBytes, &tm_q, full, k * kBK, t0);
+                    tc::tma_load_2d_pair(sm + Ly::OFF_B + s * kOpBytes, &tm_w, full, k * kBK, n0);
                     if (issued < kStages) ++issued;
                     if (++s == kStages) {
                         s = 0;
@@ -191,8 +242,8 @@ matmul_pair_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_consta
                     if (!ok) break;
                     tc::tc_fence_after();
                     if (tc::elect_one()) {
-                        const uint64_t da = tc::smem_desc(tc::smem_u32(sm + OFF_A + s * kOpBytes), 16, 1024, tc::kLayoutSw128);
-                        const uint64_t db = tc::smem_desc(tc::smem_u32(sm + OFF_B + s * kOpBytes), 16, 1024, tc::kLayoutSw128);
+                        const uint64_t da = tc::smem_desc(tc::smem_u32(sm + Ly::OFF_A + s * kOpBytes), 16, 1024, tc::kLayoutSw128);
+                        const uint64_t db = tc::smem_desc(tc::smem_u32(sm + Ly::OFF_B + s * kOpBytes), 16, 1024, tc::kLayoutSw128);
 #pragma unroll
                         for (int kk = 0; kk < kBK / 32; ++kk)        // K = 32 codes = 32 bytes per MMA
                             tc::mma_i8_ss_pair(dacc, da + (uint64_t)(kk * 2), db + (uint64_t)(kk * 2), idesc,
@@ -217,43 +268,38 @@ matmul_pair_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_consta
         // epilogue: warp w reads TMEM lanes 32 (w % 4) .. +31, the tile's rows 128 rank + 32 (w % 4) + lane,
         // and columns half .. half + 127
         const int quarter = warp & 3, half = (warp - 2) / 4 * kRows;
-        uint8_t* out_buf = sm + OFF_OUT + (warp - 2) * kOutBytes;
+        uint8_t* out_buf = sm + Ly::OFF_OUT + (warp - 2) * Ly::OUT;
         int it = 0;
         // scales (and biases) of a tile are loaded while the one before it is worked on
-        float srow = 0.f, brow = 0.f, ccol = 0.f, bcol = 0.f;
+        float srow = 0.f, ccol = 0.f, bcol = 0.f;
         const auto load_scales = [&](long long t) {
             int n0, t0;
             if (t >= tiles) return;
             tile_at(p, t, &n0, &t0);
-            const int row = (SWAP ? n0 : t0) + (int)rank * kRows + quarter * 32 + lane;
-            const int c = n0 + half + quarter * 32 + lane;
-            const bool in = row < (SWAP ? p.N : p.T);
-            srow = in ? (SWAP ? p.s_w : p.s_t)[row] : 0.f;
-            brow = SWAP && in && p.bias ? p.bias[row] : 0.f;
-            ccol = !SWAP && c < p.N ? p.s_w[c] : 0.f;
-            bcol = !SWAP && c < p.N && p.bias ? p.bias[c] : 0.f;
+            const int row = t0 + (int)rank * kRows + quarter * 32 + lane, c = n0 + half + quarter * 32 + lane;
+            srow = row < p.T ? p.s_t[row] : 0.f;
+            ccol = c < p.N ? p.s_w[c] : 0.f;
+            bcol = c < p.N && p.bias ? p.bias[c] : 0.f;
         };
         load_scales(me);
         for (long long t = me; t < tiles; t += pairs, ++it) {
             const int a = it & 1;
             int n0, t0;
             tile_at(p, t, &n0, &t0);
-            const int row0 = (SWAP ? n0 : t0) + (int)rank * kRows + quarter * 32;
-            const float st = srow, sb = brow;
-            float* col = reinterpret_cast<float*>(sm + OFF_COL) + a * 2 * kTile;
-            if (!SWAP) {
-                // the channels' scales and biases, for every warp; the other half of the buffer
-                // may still be read by a warp that is one tile behind
-                col[half + quarter * 32 + lane] = ccol;
-                col[kTile + half + quarter * 32 + lane] = bcol;
-                tc::named_sync(1, kEpi * 32);
-            }
+            const int row0 = t0 + (int)rank * kRows + quarter * 32;
+            const float st = srow;
+            float* col = reinterpret_cast<float*>(sm + Ly::OFF_COL) + a * 2 * kTile;
+            // the channels' scales and biases, for every warp; the other half of the buffer may
+            // still be read by a warp that is one tile behind
+            col[half + quarter * 32 + lane] = ccol;
+            col[kTile + half + quarter * 32 + lane] = bcol;
+            tc::named_sync(1, kEpi * 32);
             load_scales(t + pairs);
             const uint32_t trow = tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(a * kTile + half);
             const bool ok = tc::wait_or_abort(bar + B_AFULL + a, ((uint32_t)(it >> 1)) & 1, abort_flag, p.status,
                                               kStatusTimeout);
             // the warps stay together: the named barrier above counts all of them
-            if (!(SWAP ? __all_sync(0xffffffffu, ok) : tc::named_and(2, kEpi * 32, ok))) break;
+            if (!tc::named_and(2, kEpi * 32, ok)) break;
             tc::tc_fence_after();
             // this warp's part of the accumulator to registers, and the accumulator back to the MMA warp
             uint32_t v[4][32];
@@ -263,15 +309,15 @@ matmul_pair_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_consta
             tc::tc_fence_before();
             __syncwarp();
             if (lane == 0) tc::mbar_arrive_cluster(tc::map_rank(tc::smem_u32(bar + B_AEMPTY + a), 0));
-            if (SWAP) {
-                const int row = row0 + lane;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int c = t0 + half + i * 32;
-                    store_tokens(v[i], p.s_t + c, st, sb, p.out + (long long)c * p.N + row, p.N, p.T - c, lane,
-                                 row < p.N);
-                }
-            } else if (row0 < p.T && n0 + half < p.N) {
+            if (row0 >= p.T || n0 + half >= p.N) continue;
+            if (!ALIGNED) {
+                uint16_t* dst = p.out + (long long)(row0 + lane) * p.N + n0 + half;
+                const int rows = min(32, p.T - row0), cols = p.N - n0 - half;
+                store_shifted(v[0], v[1], st, col + half, col + kTile + half, out_buf, lane, dst, rows, min(64, cols));
+                if (cols > 64)
+                    store_shifted(v[2], v[3], st, col + half + 64, col + kTile + half + 64, out_buf, lane, dst + 64, rows,
+                                  min(64, cols - 64));
+            } else {
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const int c = half + i * 32;
@@ -288,7 +334,7 @@ matmul_pair_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_consta
                 }
             }
         }
-        if (!SWAP && lane == 0) tc::tma_store_wait0();            // the stores have read shared memory and are done
+        if (ALIGNED && lane == 0) tc::tma_store_wait0();            // the stores have read shared memory and are done
         __syncwarp();
     }
     tc::tc_fence_before();
@@ -297,16 +343,16 @@ matmul_pair_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_consta
     if (warp == 1) tc::tmem_dealloc_pair(tmem, kAcc * kTile);
 }
 
-template <bool SWAP>
+template <bool ALIGNED>
 cudaError_t launch(const CUtensorMap& mq, const CUtensorMap& mw, const CUtensorMap& mo, const MatmulArgs& p,
                    cudaStream_t st) {
-    const int smem = SMEM + 1024;
-    const cudaError_t e = cudaFuncSetAttribute(matmul_pair_kernel<SWAP>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    const int smem = Layout<ALIGNED>::SMEM + 1024;
+    const cudaError_t e =
+        cudaFuncSetAttribute(matmul_pair_kernel<ALIGNED>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     const long long tiles = (long long)p.tiles_t * p.tiles_n;
     const int most = device_sm_count() / 2, pairs = tiles < most ? (int)tiles : most;
-    return launch_programmatic(matmul_pair_kernel<SWAP>, 2 * pairs, kWarps * 32, smem, st, 2, SWAP ? mw : mq,
-                               SWAP ? mq : mw, mo, p);
+    return launch_programmatic(matmul_pair_kernel<ALIGNED>, 2 * pairs, kWarps * 32, smem, st, 2, mq, mw, mo, p);
 }
 
 }  // namespace pair
@@ -566,7 +612,7 @@ cudaError_t launch_matmul_i8(int T, int K, int N, const int8_t* q, const float* 
     const double load = few_tiles * S > sms ? (double)few_tiles * S / sms : 1.0;
     const double few_us = 5.2 + 3.0 * (load - 1.0) + (S > 1 ? bn / 160.0 : 0.0) +
                           load * nk / S * (few::kRows + bn) / 930.0 + 0.5 * (double)N * K / 6.5e6;
-    const double pair_us = 6.5 + (double)((pair_tiles + sms / 2 - 1) / (sms / 2)) * (0.28 * nk + (N % 8 ? 5.0 : 0.0));
+    const double pair_us = 6.5 + (double)((pair_tiles + sms / 2 - 1) / (sms / 2)) * (0.28 * nk + (N % 8 ? 2.2 : 0.0));
     if (T <= 64 || few_us <= pair_us) {
         p.tiles_n = tiles_of(N, few::kRows);
         p.tiles_t = tiles_of(T, bn);
@@ -579,12 +625,12 @@ cudaError_t launch_matmul_i8(int T, int K, int N, const int8_t* q, const float* 
     if (!operand_map(&mw, Wq, N, K, pair::kRows) || !operand_map(&mq, q, T, K, pair::kRows)) return cudaErrorInvalidValue;
     p.tiles_n = tiles_of(N, pair::kTile);
     p.tiles_t = tiles_of(T, pair::kTile);
-    if (N % 8 != 0) return pair::launch<true>(mq, mw, mq, p, st);      // the third map is not read
+    if (N % 8 != 0) return pair::launch<false>(mq, mw, mq, p, st);     // the third map is not read
     CUtensorMap mo;
     if (!make_tmap_2d(&mo, false, out, (unsigned long long)N, (unsigned long long)T, (unsigned long long)N * 2, 32, 32,
                       CU_TENSOR_MAP_SWIZZLE_64B))
         return cudaErrorInvalidValue;
-    return pair::launch<false>(mq, mw, mo, p, st);
+    return pair::launch<true>(mq, mw, mo, p, st);
 }
 
 }  // namespace ssd

@@ -182,7 +182,8 @@ def test_norm_rows_of_zeros_and_rows_that_are_not_finite(torch_cuda, d):
 
 MM = [(1, 16, 1), (1, 2560, 10576), (8, 2560, 10576), (7, 5120, 2560), (33, 144, 130), (64, 1024, 257), (65, 512, 512),
       (128, 128, 128), (129, 2064, 1000), (300, 4096, 777), (257, 400, 2049), (1001, 1040, 600), (2000, 256, 4096),
-      (2500, 272, 2305), (1001, 8192, 4096)]
+      (2500, 272, 2305), (1001, 8192, 4096),
+      (8001, 1024, 1025), (8001, 1024, 1026), (8001, 1024, 1031), (8001, 1024, 1100), (8001, 1024, 1064)]
 
 
 @pytest.mark.parametrize("T,K,N", MM)
