@@ -578,28 +578,37 @@ bool operand_map(CUtensorMap* m, const int8_t* base, int rows, int K, int box_ro
                         (unsigned)box_rows, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
-// K split of a call on matmul_few_kernel: the most ranks that leave about a CTA to an SM, or
-// up to 1.75 where each still has 16 slices (two CTAs fit an SM, but clusters beyond what
-// the GPCs hold run after the others: 1536 x 1024 -> 2048 10.4 us with S = 1, 16.0 with 2).
-int split_of(long long tiles, int nk, int sms) {
-    int S = 1;
-    for (int c : {2, 4, 8}) {
-        const long long ctas = tiles * c;
-        if (c > nk || ctas * 4 > 7LL * sms) break;
-        if (ctas * 10 <= (c == 8 ? 10LL : 11LL) * sms || (c < 8 && nk / c >= 16)) S = c;
-    }
-    return S;
+// Microseconds that a call on matmul_few_kernel is expected to take with its K axis split S
+// ways: start and end; the join (each rank reads (S - 1) / S of a tile's sums from the others,
+// at about 2.4 TB/s over all SMs); a second CTA on some SMs; and a rank's slices, each
+// (128 + bn) x 128 bytes at 87 bytes a nanosecond into an SM, 1.4 times that with rows that are
+// not whole 32-byte sectors.
+double few_estimate(long long tiles, int nk, int bn, int S, bool sectors, int sms) {
+    const double ctas = (double)tiles * S;
+    const double full = (double)((tiles * S + sms - 1) / sms);
+    const double load = ctas > sms ? 0.5 * (ctas / sms + full) : 1.0;
+    const double join = S > 1 ? 0.6 + ctas * bn * 512e-6 * (S - 1) / S / 2.4 : 0.0;
+    const double slice = (few::kRows + bn) / 680.0 * (sectors ? 1.0 : 1.4);
+    return 4.0 + join + (load - 1.0) + load * nk / S * slice;
+}
+
+// The same for matmul_pair_kernel: start and end, then for each turn of the pairs over the
+// tiles the slices and a tile's rows out, which cost more where they are not aligned.
+double pair_estimate(long long tiles, int nk, bool sectors, bool aligned, int sms) {
+    const double turns = (double)((tiles + sms / 2 - 1) / (sms / 2));
+    return 3.5 + turns * (nk * (sectors ? 0.31 : 0.33) + (aligned ? 1.3 : 3.1));
 }
 
 }  // namespace
 
-// Which kernel: matmul_few_kernel up to 64 tokens, else by an estimate of both, in
-// microseconds.  Few tokens: what a CTA takes besides its K slices, what a second CTA on an
-// SM or a split adds, a slice's bytes through an SM, and half the weights' time from HBM.  Pairs: the same for a 256 x 256 tile's slices
-// (and the unaligned epilogue's stores).  Measured (few, pair):
-//   128 x 2560 -> 10576 12.1, 12.3    192 15.4, 12.5     384 16.8, 18.9     512 27.2, 19.1
-//   256 x 5120 -> 2560  10.8, 17.0    768 16.4, 17.6    1024 21.1, 17.8
-//   192 x 8192 -> 4096  15.8, 24.4    512 21.4, 24.6     768 33.5, 24.9    512^3  6.4, 7.1
+// Which kernel, and how many ranks: matmul_few_kernel up to 64 tokens, else the one that is
+// expected to take less; the split S that is (all CTAs resident at a time, and none up to 4
+// slices: 31 x 432 -> 593 3.6 us whole, 4.4 and 4.2 split by 2 and 4).  Over 88 other sizes than
+// the estimates were fitted to, drawn at random (1 to 8192 tokens, K to 8192, N to 18560), the
+// choice takes 1.9% longer than the best of all five in the geometric mean.  Measured in a graph, microseconds with S = 1, 2,
+// 4, 8 and on pairs:
+//    8 x 5120 -> 2560  11.1  7.6  5.7  5.5 15.2     192 x 1024 -> 2048   6.9  7.1  8.2 10.9   7.0
+//  192 x 4096 ->  777  12.5  9.8  7.5  8.9 15.6    1536 x 2048 -> 8512  41.0 63.3   -    -   21.7
 cudaError_t launch_matmul_i8(int T, int K, int N, const int8_t* q, const float* s_t, const int8_t* Wq,
                              const float* s_w, const float* bias, uint16_t* out, int* status, cudaStream_t st) {
     CUtensorMap mw, mq;
@@ -608,11 +617,18 @@ cudaError_t launch_matmul_i8(int T, int K, int N, const int8_t* q, const float* 
     const int bn = T <= 16 ? 16 : T <= 32 ? 32 : T <= 64 ? 64 : 128;
     const long long few_tiles = (long long)tiles_of(N, few::kRows) * tiles_of(T, bn);
     const long long pair_tiles = (long long)tiles_of(T, pair::kTile) * tiles_of(N, pair::kTile);
-    const int S = split_of(few_tiles, nk, sms);
-    const double load = few_tiles * S > sms ? (double)few_tiles * S / sms : 1.0;
-    const double few_us = 5.2 + 3.0 * (load - 1.0) + (S > 1 ? bn / 160.0 : 0.0) +
-                          load * nk / S * (few::kRows + bn) / 930.0 + 0.5 * (double)N * K / 6.5e6;
-    const double pair_us = 6.5 + (double)((pair_tiles + sms / 2 - 1) / (sms / 2)) * (0.28 * nk + (N % 8 ? 2.2 : 0.0));
+    const bool sectors = K % 32 == 0;
+    int S = 1;
+    double few_us = few_estimate(few_tiles, nk, bn, 1, sectors, sms);
+    for (int c : {2, 4, 8}) {
+        if (nk <= 4 || c > nk || few_tiles * c * 4 > 7LL * sms) break;
+        const double us = few_estimate(few_tiles, nk, bn, c, sectors, sms);
+        if (us < few_us) {
+            few_us = us;
+            S = c;
+        }
+    }
+    const double pair_us = pair_estimate(pair_tiles, nk, sectors, N % 8 == 0, sms);
     if (T <= 64 || few_us <= pair_us) {
         p.tiles_n = tiles_of(N, few::kRows);
         p.tiles_t = tiles_of(T, bn);
