@@ -354,14 +354,14 @@ ssd_status ssd_gated_rmsnorm_i8(int tokens, int d, const uint16_t* y, const uint
 
 /* INT8 matrix product with a scale per token and per output channel (a projection):
  *   out[t,n] = s_t[t] * s_w[n] * sum_k q[t,k] * Wq[n,k] + bias[n]       (bf16)
- * The sum is exact in INT32 (k <= 131072); the scaling is fp32, rounded once to bf16.
+ * The sum is exact in INT32 (k <= 131056, all codes -128 too); the scaling is fp32, rounded once to bf16.
  * q : device int8 [tokens, k]     s_t : device fp32 [tokens]
  * Wq : device int8 [n, k]         s_w : device fp32 [n]      bias : device fp32 [n] or null
  * out : device bf16 [tokens, n], written
  * status : device int, left alone unless a device-side bounded wait expires, which writes
  *   SSD_ERR_TIMEOUT: clear it once, read it with ssd_workspace_status(status, stream).  Calls
  *   may share it.
- * k % 16 == 0, k <= 131072, 0 <= tokens <= 2^30 and 1 <= n <= 2^30, else
+ * k % 16 == 0, k <= 131056, 0 <= tokens <= 2^30 and 1 <= n <= 2^30, else
  * SSD_ERR_UNSUPPORTED (negative: SSD_ERR_INVALID_ARG). */
 ssd_status ssd_matmul_i8(int tokens, int k, int n, const int8_t* q, const float* s_t, const int8_t* Wq,
                          const float* s_w, const float* bias, uint16_t* out, int* status, cudaStream_t stream);

@@ -531,9 +531,9 @@ ssd_status ssd_gated_rmsnorm_i8(int tokens, int d, const uint16_t* y, const uint
 ssd_status ssd_matmul_i8(int tokens, int k, int n, const int8_t* q, const float* s_t, const int8_t* Wq,
                          const float* s_w, const float* bias, uint16_t* out, int* status, cudaStream_t stream) {
     if (tokens < 0 || k < 1 || n < 1) return SSD_ERR_INVALID_ARG;
-    // rows of codes are TMA rows (16-byte strides); |sum| <= k * 127^2 stays in INT32; row
+    // rows of codes are TMA rows (16-byte strides); |sum| <= k * 128^2 stays in INT32; row
     // numbers past a tile's end stay in an int
-    if (k % 16 != 0 || k > 131072 || tokens > (1 << 30) || n > (1 << 30)) return SSD_ERR_UNSUPPORTED;
+    if (k % 16 != 0 || k > 131056 || tokens > (1 << 30) || n > (1 << 30)) return SSD_ERR_UNSUPPORTED;
     if (tokens == 0) return SSD_OK;
     if (!q || !s_t || !Wq || !s_w || !out || !status) return SSD_ERR_INVALID_ARG;
     if (!aligned16(q) || !aligned16(s_t) || !aligned16(Wq) || !aligned16(s_w) || !aligned16(bias) || !aligned16(out) ||

@@ -128,7 +128,7 @@ __device__ __forceinline__ void load8(const float* p, f32x2 (&f)[4]) {
 }
 
 // silu(u) = u / (1 + exp(-u)) from the fast exponential and reciprocal, a relative error of
-// a few 2^-23 times 1 + |u|: u below -88 gives -0, NaN stays NaN.
+// a few 2^-23 times 1 + |u|: u below -87 gives -0, NaN stays NaN.
 __device__ __forceinline__ f32x2 fast_silu2(f32x2 u) {
     const float2 t = split2(mul2(u, both2(-1.4426950408889634f)));
     float2 e, r;

@@ -112,6 +112,22 @@ def test_steps_follow_a_prompt(torch_cuda):
 
 
 @pytest.mark.parametrize("path", ["bf16", "w8a8"])
+def test_prompts_without_tokens_leave_the_state(torch_cuda, path):
+    """No tokens at all, and a padded batch of rows that are all padding."""
+    torch = torch_cuda
+    layer = _layer(torch, path)
+    start = {"conv": _hidden(torch, 6, 2, W - 1, H * P + 2 * G * N), "ssd": layer.zero_state(2)["ssd"].random_(-100, 100)}
+    for state in (None, start):
+        want = layer.zero_state(2) if state is None else start
+        out, kept, got = layer.prefill(_hidden(torch, 1, 2, 0, D), None, state)
+        assert out.shape == kept.shape == (2, 0, D) and kept.dtype == torch.float32
+        assert all(torch.equal(got[k], want[k]) for k in want)
+        _, _, got = layer.prefill(_hidden(torch, 1, 2, 9, D), None, state,
+                                  torch.zeros(2, dtype=torch.int32, device="cuda"))
+        assert all(torch.equal(got[k], want[k]) for k in want)
+
+
+@pytest.mark.parametrize("path", ["bf16", "w8a8"])
 def test_padded_batch_equals_its_rows(torch_cuda, path):
     torch = torch_cuda
     layer = _layer(torch, path)

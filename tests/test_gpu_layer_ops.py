@@ -210,21 +210,22 @@ def test_matmul(torch_cuda, T, K, N, biased):
     assert (off <= lim).all(), (off / lim).max()
 
 
-def test_matmul_extreme_sums_stay_exact(torch_cuda):
-    """All codes 127 over the longest k: the sum 131072 * 127^2 fits INT32."""
+@pytest.mark.parametrize("code", [127, -128])
+def test_matmul_extreme_sums_stay_exact(torch_cuda, code):
+    """All codes the largest over the longest k: the sum 131056 * 128^2 fits INT32, the next k's would not."""
     torch = torch_cuda
     import int8_quant_b200 as iq
     for T in (3, 200):
-        K, N = 131072, 160
-        q = torch.full((T, K), 127, dtype=torch.int8, device="cuda")
-        Wq = torch.full((N, K), -127, dtype=torch.int8, device="cuda")
-        Wq[::2] = 127
+        K, N = 131056, 160
+        q = torch.full((T, K), code, dtype=torch.int8, device="cuda")
+        Wq = torch.full((N, K), 127 if code < 0 else -127, dtype=torch.int8, device="cuda")
+        Wq[::2] = code
         one = lambda n: torch.full((n,), 2.0 ** -15, device="cuda")  # noqa: E731
         out, st = torch.empty(T, N, device="cuda").bfloat16(), torch.zeros(1, dtype=torch.int32, device="cuda")
         iq.ssd_matmul_i8(q, one(T), Wq, one(N), None, out, st)
-        want = 131072 * 127 * 127 * 2.0 ** -30
+        want, other = K * code * code * 2.0 ** -30, -K * abs(code) * 127 * 2.0 ** -30
         got = _np(torch, out)
-        assert np.abs(got[:, ::2] / want - 1).max() <= H and np.abs(got[:, 1::2] / want + 1).max() <= H
+        assert np.abs(got[:, ::2] / want - 1).max() <= H and np.abs(got[:, 1::2] / other - 1).max() <= H
 
 
 def test_matmul_carries_a_poisoned_scale(torch_cuda):

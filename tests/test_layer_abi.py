@@ -40,7 +40,8 @@ def test_matmul_refusals():
     f = iq.library().ssd_matmul_i8
     good = [4, 64, 8, F, F, F, F, F, F, F, None]
     for i, v, want in [(0, -1, INVALID), (1, 0, INVALID), (2, 0, INVALID), (1, 40, UNSUPPORTED),
-                       (1, 131088, UNSUPPORTED), (0, 2 ** 30 + 1, UNSUPPORTED), (2, 2 ** 30 + 1, UNSUPPORTED), (3, None, INVALID), (3, ODD, INVALID), (4, None, INVALID),
+                       (1, 131072, UNSUPPORTED), (0, 2 ** 30 + 1, UNSUPPORTED), (2, 2 ** 30 + 1, UNSUPPORTED),
+                       (3, None, INVALID), (3, ODD, INVALID), (4, None, INVALID),
                        (5, None, INVALID), (6, None, INVALID), (7, ODD, INVALID), (8, None, INVALID), (8, ODD, INVALID),
                        (9, None, INVALID)]:
         a = list(good)
