@@ -363,7 +363,15 @@ namespace few {
 
 constexpr int kRows = 128;                            // channels of a tile
 constexpr int kMaxStages = 12;
-constexpr int kBudget = 98304;                        // shared memory for stages: two CTAs an SM
+// Shared memory for stages where two CTAs share an SM, and where none has to: the bytes on
+// their way bound an SM's rate (8 x 4096 -> 18560 from HBM 14.5 us with 96 KB, 13.7 with 148;
+// 64 x 4096 -> 2048 6.6, 5.8).  148 KB leave room for the CTAs of the next kernel.
+constexpr int kBudget = 98304, kBudgetAlone = 151552;
+// Slices that go to L2 ahead of the wait for the previous kernel.  All of them are as many
+// requests again in front of the first load (8 x 4096 -> 18560 20.5 us); a decode step of a
+// layer of 2560 features (5120 channels, batch 8) takes 26.4 us with all, 27.4, 26.6, 26.2,
+// 26.2 and 26.4 with 2, 4, 6, 8 and 10.
+constexpr int kAhead = 6;
 constexpr int B_FULL = 0, B_EMPTY = kMaxStages, B_DONE = 2 * kMaxStages, NBAR = B_DONE + 1;
 constexpr int OFF_FLAG = NBAR * 8, OFF_TMEM = OFF_FLAG + 8, OFF_BUF = 1024;
 static_assert(OFF_TMEM + 8 <= OFF_BUF, "barriers in front of the stages");
@@ -372,7 +380,7 @@ template <int BN>
 struct Layout {
     static constexpr int A_BYTES = kRows * kBK, B_BYTES = BN * kBK, STAGE = A_BYTES + B_BYTES;
     static constexpr int RED = BN * kRows * 4;                    // partial sums, over the stages
-    static constexpr int MOST = kBudget / STAGE < kMaxStages ? kBudget / STAGE : kMaxStages;
+    static constexpr int most(int budget) { return budget / STAGE < kMaxStages ? budget / STAGE : kMaxStages; }
     static constexpr int COLS = BN < 32 ? 32 : BN;                // TMEM columns
     // with `stages` of them, and room to align the first
     static int smem(int stages) { return 1024 + OFF_BUF + (stages * STAGE > RED ? stages * STAGE : RED); }
@@ -411,8 +419,8 @@ matmul_few_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constan
         tc::fence_proxy_async_smem();
         tc::prefetch_tmap(&tm_w);
         tc::prefetch_tmap(&tm_q);
-        // the weights on their way to L2 while the kernel ahead in the stream ends
-        for (int j = 0; j < k1 - k0; ++j) tc::tma_prefetch_2d(&tm_w, (k0 + j) * kBK, n0);
+        // the first weights on their way to L2 while the kernel ahead in the stream ends
+        for (int j = 0; j < min(kAhead, k1 - k0); ++j) tc::tma_prefetch_2d(&tm_w, (k0 + j) * kBK, n0);
         grid_wait();
         for (int j = 0; j < first; ++j) load(j, j);
     }
@@ -557,16 +565,23 @@ matmul_few_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constan
     if (warp == 1) tc::tmem_dealloc(tmem, Ly::COLS);
 }
 
+// Whether each CTA of a call has an SM to itself.  Clusters of more than two leave some SMs of
+// their part of the GPU unused (35 of four with an SM a CTA run in two turns: 5 x 4464 -> 4480
+// 13.0 us, 8.0 with two CTAs an SM).
+bool alone(long long ctas, int S, int sms) { return ctas * 8 <= sms * (S > 2 ? 7LL : 8LL); }
+
 template <int BN>
 cudaError_t launch(const CUtensorMap& mw, const CUtensorMap& mq, const MatmulArgs& p, int S, cudaStream_t st) {
     using Ly = Layout<BN>;
     const cudaError_t e =
-        cudaFuncSetAttribute(matmul_few_kernel<BN>, cudaFuncAttributeMaxDynamicSharedMemorySize, Ly::smem(Ly::MOST));
+        cudaFuncSetAttribute(matmul_few_kernel<BN>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             Ly::smem(Ly::most(kBudgetAlone)));
     if (e != cudaSuccess) return e;
-    const int nk = (p.K - 1) / kBK + 1, most = (nk - 1) / S + 1;   // a rank's slices
-    const int stages = most < Ly::MOST ? most : Ly::MOST;
-    return launch_programmatic(matmul_few_kernel<BN>, (unsigned)((long long)p.tiles_n * p.tiles_t * S), kWarps * 32,
-                               Ly::smem(stages), st, S, mw, mq, p, S, stages);
+    const long long ctas = (long long)p.tiles_n * p.tiles_t * S;
+    const int most = Ly::most(alone(ctas, S, device_sm_count()) ? kBudgetAlone : kBudget);
+    const int nk = (p.K - 1) / kBK + 1, slices = (nk - 1) / S + 1;   // a rank's
+    return launch_programmatic(matmul_few_kernel<BN>, (unsigned)ctas, kWarps * 32, Ly::smem(slices < most ? slices : most),
+                               st, S, mw, mq, p, S, slices < most ? slices : most);
 }
 
 }  // namespace few
@@ -578,37 +593,39 @@ bool operand_map(CUtensorMap* m, const int8_t* base, int rows, int K, int box_ro
                         (unsigned)box_rows, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
-// Microseconds that a call on matmul_few_kernel is expected to take with its K axis split S
-// ways: start and end; the join (each rank reads (S - 1) / S of a tile's sums from the others,
-// at about 2.4 TB/s over all SMs); a second CTA on some SMs; and a rank's slices, each
-// (128 + bn) x 128 bytes at 87 bytes a nanosecond into an SM, 1.4 times that with rows that are
-// not whole 32-byte sectors.
+// Microseconds that a call on matmul_few_kernel is expected to take, its weights in HBM, with its
+// K axis split S ways: start, end and a tile's rows out; the join (each rank reads (S - 1) / S of
+// a tile's sums from the others, at about 2.4 TB/s over all SMs); and a rank's slices, each
+// (128 + bn) x 128 bytes at 96 bytes a nanosecond into an SM that holds one CTA, 38 for each of
+// two, 1.2 times that with rows that are not whole 32-byte sectors.
 double few_estimate(long long tiles, int nk, int bn, int S, bool sectors, int sms) {
-    const double ctas = (double)tiles * S;
-    const double full = (double)((tiles * S + sms - 1) / sms);
-    const double load = ctas > sms ? 0.5 * (ctas / sms + full) : 1.0;
-    const double join = S > 1 ? 0.6 + ctas * bn * 512e-6 * (S - 1) / S / 2.4 : 0.0;
-    const double slice = (few::kRows + bn) / 680.0 * (sectors ? 1.0 : 1.4);
-    return 4.0 + join + (load - 1.0) + load * nk / S * slice;
+    const long long ctas = tiles * S;
+    const double slices = (double)nk / S * (few::kRows + bn) * (sectors ? 1.0 : 1.2);
+    const double fixed = 2.4 + 1.2 * bn / 128 +
+                         (S > 1 ? 0.5 + 0.1 * S + (double)ctas * bn * 512e-6 * (S - 1) / S / 2.4 : 0.0);
+    if (few::alone(ctas, S, sms)) return fixed + slices / 750.0;
+    double turns = (double)ctas / (2 * sms);
+    turns = turns <= 1.0 ? 1.0 : 0.5 * (turns + (double)((ctas - 1) / (2 * sms) + 1));
+    return fixed + turns * slices / 300.0 + (turns - 1.0) * 4.0;
 }
 
 // The same for matmul_pair_kernel: start and end, then for each turn of the pairs over the
 // tiles the slices and a tile's rows out, which cost more where they are not aligned.
 double pair_estimate(long long tiles, int nk, bool sectors, bool aligned, int sms) {
     const double turns = (double)((tiles + sms / 2 - 1) / (sms / 2));
-    return 3.5 + turns * (nk * (sectors ? 0.31 : 0.33) + (aligned ? 1.3 : 3.1));
+    return 3.3 + turns * (nk * (sectors ? 0.30 : 0.36) + (aligned ? 1.9 : 3.9));
 }
 
 }  // namespace
 
 // Which kernel, and how many ranks: matmul_few_kernel up to 64 tokens, else the one that is
 // expected to take less; the split S that is (all CTAs resident at a time, and none up to 4
-// slices: 31 x 432 -> 593 3.6 us whole, 4.4 and 4.2 split by 2 and 4).  Over 88 other sizes than
-// the estimates were fitted to, drawn at random (1 to 8192 tokens, K to 8192, N to 18560), the
-// choice takes 1.9% longer than the best of all five in the geometric mean.  Measured in a graph, microseconds with S = 1, 2,
-// 4, 8 and on pairs:
-//    8 x 5120 -> 2560  11.1  7.6  5.7  5.5 15.2     192 x 1024 -> 2048   6.9  7.1  8.2 10.9   7.0
-//  192 x 4096 ->  777  12.5  9.8  7.5  8.9 15.6    1536 x 2048 -> 8512  41.0 63.3   -    -   21.7
+// slices: 31 x 432 -> 593 3.6 us whole, 4.4 and 4.2 split by 2 and 4).  Over 150 other sizes than
+// the estimates were fitted to, drawn at random (1 to 1024 tokens, K to 8192, N to 18560), the
+// choice takes 1.5% longer than the best of all in the geometric mean.  Measured in a graph, each
+// call's weights in HBM, microseconds with S = 1, 2, 4, 8 and on pairs:
+//    8 x 5120 -> 2560  11.3  7.6  6.2  6.0 15.7      64 x 4096 -> 2048  10.4  7.8  6.3  6.8  13.7
+//    8 x 8192 -> 4096  16.8 10.8  9.4  8.7 23.9     512 x 8192 -> 4096  22.8 20.1 29.7 50.0  23.7
 cudaError_t launch_matmul_i8(int T, int K, int N, const int8_t* q, const float* s_t, const int8_t* Wq,
                              const float* s_w, const float* bias, uint16_t* out, int* status, cudaStream_t st) {
     CUtensorMap mw, mq;
