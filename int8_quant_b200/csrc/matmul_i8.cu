@@ -10,9 +10,14 @@
 //                       shared memory, by TMA where n % 8 == 0; otherwise no row of the output
 //                       is aligned, and each is stored from a copy that is shifted in shared
 //                       memory until their 16-byte vectors match.
-//   matmul_few_kernel   few tokens or few tiles: one 128-channel tile (rows) of up to 128
-//                       tokens per cluster, the K axis split over the cluster's CTAs and
-//                       the INT32 partial sums joined through distributed shared memory.
+//   matmul_few_kernel   few tokens or few tiles: one tile of up to 128 channels (rows) and up to
+//                       128 tokens per cluster, the K axis split over the cluster's CTAs and
+//                       the INT32 partial sums joined through distributed shared memory.  Bound
+//                       by the weights' way in: a barrier's answer takes some 60 cycles and a
+//                       slice's MMAs 130, so that one warp that loads and one that issues spent
+//                       450 cycles a slice, whatever its bytes.  Two of each spend under 200
+//                       (unsplit 8 x 5120 -> 2560, from L2: 11.5 us with one, 9.2 with two that
+//                       issue, 6.9 with two that load as well).
 //
 // Every wait is bounded; an expired wait raises the CTA's abort flag and records
 // SSD_ERR_TIMEOUT in the status word.
@@ -36,6 +41,8 @@ struct MatmulArgs {
     const float* bias;
     uint16_t* out;
     int* status;
+    int rows;                   // channels of a tile of matmul_few_kernel
+    const int8_t* Wq;           // for it to prefetch
 };
 
 // ---------------------------------------------------------------- many tokens: CTA pairs
@@ -361,29 +368,41 @@ cudaError_t launch(const CUtensorMap& mq, const CUtensorMap& mw, const CUtensorM
 
 namespace few {
 
-constexpr int kRows = 128;                            // channels of a tile
-constexpr int kMaxStages = 12;
+constexpr int kRows = 128;                            // rows of the MMA; a tile has up to as many channels
+constexpr int kMaxStages = 16, kLeastRows = 64;
+// Lines that a CTA prefetches at most (8 x 4096 -> 18560 14.6 us with all 4096, 13.6 so; 64 tokens
+// 17.2, 15.3; 64 x 5120 -> 2560 7.0 with 768, 6.6 with all its 1280).
+constexpr int kAhead = 1280;
+constexpr int kLoader2 = 3;                           // the second loading warp, until its epilogue
 // Shared memory for stages where two CTAs share an SM, and where none has to: the bytes on
 // their way bound an SM's rate (8 x 4096 -> 18560 from HBM 14.5 us with 96 KB, 13.7 with 148;
 // 64 x 4096 -> 2048 6.6, 5.8).  148 KB leave room for the CTAs of the next kernel.
 constexpr int kBudget = 98304, kBudgetAlone = 151552;
-// Slices that go to L2 ahead of the wait for the previous kernel.  All of them are as many
-// requests again in front of the first load (8 x 4096 -> 18560 20.5 us); a decode step of a
-// layer of 2560 features (5120 channels, batch 8) takes 26.4 us with all, 27.4, 26.6, 26.2,
-// 26.2 and 26.4 with 2, 4, 6, 8 and 10.
-constexpr int kAhead = 6;
 constexpr int B_FULL = 0, B_EMPTY = kMaxStages, B_DONE = 2 * kMaxStages, NBAR = B_DONE + 1;
 constexpr int OFF_FLAG = NBAR * 8, OFF_TMEM = OFF_FLAG + 8, OFF_BUF = 1024;
 static_assert(OFF_TMEM + 8 <= OFF_BUF, "barriers in front of the stages");
 
 template <int BN>
 struct Layout {
-    static constexpr int A_BYTES = kRows * kBK, B_BYTES = BN * kBK, STAGE = A_BYTES + B_BYTES;
     static constexpr int RED = BN * kRows * 4;                    // partial sums, over the stages
-    static constexpr int most(int budget) { return budget / STAGE < kMaxStages ? budget / STAGE : kMaxStages; }
-    static constexpr int COLS = BN < 32 ? 32 : BN;                // TMEM columns
-    // with `stages` of them, and room to align the first
-    static int smem(int stages) { return 1024 + OFF_BUF + (stages * STAGE > RED ? stages * STAGE : RED); }
+    // Warps that issue MMAs, and that load.  With 128 tokens a slice's MMAs take as long as the
+    // barriers, and three stages of 32 KB are no two pairs.
+    static constexpr int ISSUE = BN <= 64 ? 2 : 1;
+    static constexpr int COLS = ISSUE * BN;                       // TMEM columns, a power of two from 32
+    // A stage has `rows` rows of weights and BN of tokens.  The MMA reads 128 rows: what lies behind
+    // the weights' own makes sums that nobody reads.
+    static __host__ __device__ constexpr int stage(int rows) { return (rows + BN) * kBK; }
+    static constexpr int behind(int rows) { return kRows > rows + BN ? (kRows - rows - BN) * kBK : 0; }
+    static int stages(int rows, int slices, int budget) {
+        int n = (budget - behind(rows)) / stage(rows);
+        if (n > kMaxStages) n = kMaxStages;
+        return n >= slices ? slices : n / ISSUE * ISSUE;          // a stage keeps to one issuing warp
+    }
+    // with room to align the first
+    static int smem(int rows, int n) {
+        const int bytes = n * stage(rows) + behind(rows);
+        return 1024 + OFF_BUF + (bytes > RED ? bytes : RED);
+    }
 };
 
 // Cluster rank r takes the K slices [r nk / S, (r + 1) nk / S) of the tile (channels n0 ..,
@@ -403,26 +422,33 @@ matmul_few_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constan
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = S > 1 ? (int)tc::cluster_rank() : 0;
     const int tile = blockIdx.x / S;
-    const int n0 = (tile % p.tiles_n) * kRows, t0 = (tile / p.tiles_n) * BN;
+    const int n0 = (tile % p.tiles_n) * p.rows, t0 = (tile / p.tiles_n) * BN;
+    const int stage = Ly::stage(p.rows);
     const int nk = (p.K + kBK - 1) / kBK;
     const int k0 = (int)((long long)rank * nk / S), k1 = (int)((long long)(rank + 1) * nk / S);
     const int first = min(stages, k1 - k0);                       // slices loaded before anything waits
     const auto load = [&](int j, int s) {
-        tc::mbar_arrive_expect_tx(bar + B_FULL + s, Ly::STAGE);
-        tc::tma_load_2d(buf + s * Ly::STAGE, &tm_w, bar + B_FULL + s, (k0 + j) * kBK, n0);
-        tc::tma_load_2d(buf + s * Ly::STAGE + Ly::A_BYTES, &tm_q, bar + B_FULL + s, (k0 + j) * kBK, t0);
+        tc::mbar_arrive_expect_tx(bar + B_FULL + s, stage);
+        tc::tma_load_2d(buf + s * stage, &tm_w, bar + B_FULL + s, (k0 + j) * kBK, n0);
+        tc::tma_load_2d(buf + s * stage + p.rows * kBK, &tm_q, bar + B_FULL + s, (k0 + j) * kBK, t0);
     };
     if (threadIdx.x == 0) {
-        for (int i = 0; i < NBAR; ++i) tc::mbar_init(bar + i, 1);
+        for (int i = 0; i < NBAR; ++i) tc::mbar_init(bar + i, i == B_DONE ? Ly::ISSUE : 1);
         *abort_flag = 0;
         tc::fence_mbar_init();
         tc::fence_proxy_async_smem();
         tc::prefetch_tmap(&tm_w);
         tc::prefetch_tmap(&tm_q);
-        // the first weights on their way to L2 while the kernel ahead in the stream ends
-        for (int j = 0; j < min(kAhead, k1 - k0); ++j) tc::tma_prefetch_2d(&tm_w, (k0 + j) * kBK, n0);
         grid_wait();
         for (int j = 0; j < first; ++j) load(j, j);
+    }
+    // The weights on their way to L2 while the kernel ahead in the stream ends, a line a thread (no
+    // value is read: what is written in between is seen).  TMA's prefetches would stand in front of
+    // its loads (8 x 4096 -> 18560 20.5 us).
+    if (warp >= 2) {
+        for (int k = k0; k < min(k1, k0 + kAhead / p.rows); ++k)
+            for (int r = (int)threadIdx.x - 64; r < min(p.rows, p.N - n0); r += kEpi * 32)
+                asm volatile("prefetch.global.L2 [%0];" ::"l"(p.Wq + (long long)(n0 + r) * p.K + k * kBK));
     }
     if (warp == 1) {
         tc::tmem_alloc(tmem_slot, Ly::COLS);
@@ -436,59 +462,74 @@ matmul_few_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constan
     const uint32_t tmem = *tmem_slot;
 
     bool ok = true;
-    if (warp == 0) {
-        if (lane == 0) {
-            int j = first, s = 0;
+    if (warp == 0 || warp == kLoader2) {
+        if (lane == 0 && (warp == 0 || Ly::ISSUE > 1)) {
+            // each loading warp refills the stages of one issuing warp
+            int j = first + (warp == 0 ? 0 : 1), s = j - first;
             uint32_t phase = 0;                                   // of the stage's previous use
-            for (; j < k1 - k0; ++j) {
-                if (!(ok = tc::wait_or_abort(bar + B_EMPTY + s, phase, abort_flag, p.status, kStatusTimeout))) break;
-                load(j, s);
-                if (++s == stages) {
-                    s = 0;
+            bool ready = false;                                   // asked a slice ahead: an answer takes a while
+            for (; j < k1 - k0; j += Ly::ISSUE) {
+                if (!ready && !(ok = tc::wait_or_abort(bar + B_EMPTY + s, phase, abort_flag, p.status, kStatusTimeout)))
+                    break;
+                const int at = s;
+                if ((s += Ly::ISSUE) >= stages) {
+                    s -= stages;
                     phase ^= 1;
                 }
+                ready = j + Ly::ISSUE < k1 - k0 && tc::mbar_test(bar + B_EMPTY + s, phase);
+                load(j, at);
             }
             if (!ok)                                              // the copies in flight land before the CTA ends
-                for (int i = max(0, j - stages); i < j; ++i)
+                for (int i = j - stages; i < j; i += Ly::ISSUE)
                     tc::mbar_wait(bar + B_FULL + i % stages, ((uint32_t)(i / stages)) & 1, kDrainLimit);
         }
         __syncwarp();
-    } else if (warp == 1) {
+    } else if (warp <= Ly::ISSUE) {
+        // each of the issuing warps takes every Ly::ISSUE-th slice, into sums of its own
         const uint32_t idesc = tc::idesc_s8_s32(kRows, BN, tc::kMajorK, tc::kMajorK);
-        int s = 0;
+        const uint32_t acc = tmem + (uint32_t)((warp - 1) * BN);
+        const uint64_t da0 = tc::smem_desc(tc::smem_u32(buf), 16, 1024, tc::kLayoutSw128);
+        const uint32_t da = (uint32_t)da0, hi = (uint32_t)(da0 >> 32), db = da + (uint32_t)(p.rows * kBK >> 4);
+        const bool lead = tc::elect_one();
+        int s = warp - 1;
         uint32_t phase = 0;
-        for (int j = 0; j < k1 - k0; ++j) {
-            ok = __all_sync(0xffffffffu, tc::wait_or_abort(bar + B_FULL + s, phase, abort_flag, p.status,
-                                                          kStatusTimeout));
-            if (!ok) break;
-            tc::tc_fence_after();
-            if (tc::elect_one()) {
-                const uint8_t* st = buf + s * Ly::STAGE;
-                const uint64_t da = tc::smem_desc(tc::smem_u32(st), 16, 1024, tc::kLayoutSw128);
-                const uint64_t db = tc::smem_desc(tc::smem_u32(st + Ly::A_BYTES), 16, 1024, tc::kLayoutSw128);
-#pragma unroll
-                for (int kk = 0; kk < kBK / 32; ++kk)
-                    tc::mma_i8_ss(tmem, da + (uint64_t)(kk * 2), db + (uint64_t)(kk * 2), idesc, (j | kk) != 0);
-                tc::mma_commit(bar + B_EMPTY + s);
-            }
-            __syncwarp();
-            if (++s == stages) {
-                s = 0;
+        bool ready = false;                                       // asked a slice ahead: an answer takes a while
+        for (int j = warp - 1; j < k1 - k0; j += Ly::ISSUE) {
+            if (!ready && !(ok = tc::wait_or_abort(bar + B_FULL + s, phase, abort_flag, p.status, kStatusTimeout))) break;
+            const int at = s;
+            if ((s += Ly::ISSUE) >= stages) {
+                s -= stages;
                 phase ^= 1;
             }
+            ready = j + Ly::ISSUE < k1 - k0 && tc::mbar_test(bar + B_FULL + s, phase);
+            tc::tc_fence_after();
+            if (lead) {
+                const uint32_t off = (uint32_t)(at * (stage >> 4));
+#pragma unroll
+                for (int kk = 0; kk < kBK / 32; ++kk)
+                    tc::mma_i8_ss(acc, (uint64_t)hi << 32 | (da + off + kk * 2), (uint64_t)hi << 32 | (db + off + kk * 2),
+                                  idesc, j >= Ly::ISSUE || kk);
+                tc::mma_commit(bar + B_EMPTY + at);
+            }
         }
-        if (tc::elect_one()) tc::mma_commit(bar + B_DONE);          // every MMA issued, also when the loop gave up
+        ok = __all_sync(0xffffffffu, ok);
+        if (lead) tc::mma_commit(bar + B_DONE);                     // every MMA issued, also when the loop gave up
         __syncwarp();
-        if (!ok) tc::mbar_wait(bar + B_DONE, 0, kDrainLimit);
+        if (ok) ok = tc::wait_or_abort(bar + B_DONE, 0, abort_flag, p.status, kStatusTimeout);
+        else tc::mbar_wait(bar + B_DONE, 0, kDrainLimit);
+        __syncwarp();
     }
     const int quarter = warp & 3, row = quarter * 32 + lane, ch = n0 + row, part = (warp - 2) / 4;
-    const bool in = warp >= 2 && ch < p.N;
+    const bool in = warp >= 2 && row < p.rows && ch < p.N;
     const float sw = in ? p.s_w[ch] : 0.f;
     const float bias = in && p.bias ? p.bias[ch] : 0.f;
     const int live = min(BN, p.T - t0);
     int* red = reinterpret_cast<int*>(buf);
+    // the other warps wait here, not at the MMA's barrier: eight of them asking it slow every
+    // barrier of the CTA down
+    __syncthreads();
+    ok = !*abort_flag;
     if (warp >= 2) {
-        ok = __all_sync(0xffffffffu, tc::wait_or_abort(bar + B_DONE, 0, abort_flag, p.status, kStatusTimeout));
         tc::tc_fence_after();
         const uint32_t trow = tmem + ((uint32_t)(quarter * 32) << 16);
         uint16_t* dst = p.out + (long long)t0 * p.N + ch;
@@ -497,9 +538,14 @@ matmul_few_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constan
             // a CTA on its own stores what it has
 #pragma unroll 1
             for (int c = 16 * part; c < live; c += 32) {
-                uint32_t v[16];
+                uint32_t v[16], v1[16];
                 tc::tmem_ld16(trow + c, v);
+                if (Ly::ISSUE > 1 && k1 - k0 > 1) tc::tmem_ld16(trow + BN + c, v1);
                 tc::tmem_wait_ld();
+                if (Ly::ISSUE > 1 && k1 - k0 > 1) {
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) v[j] += v1[j];
+                }
                 if (S > 1) {
 #pragma unroll
                     for (int j = 0; j < 16; ++j) red[(c + j) * kRows + row] = (int)v[j];
@@ -523,13 +569,13 @@ matmul_few_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constan
         tc::cluster_sync();
         if (warp >= 2 && ok) {
             // a warp takes a token of this rank's share, a lane four channels
-            const int c4 = n0 + 4 * lane;
+            const int c4 = n0 + 4 * lane, end = min(p.N, n0 + p.rows);
             const uint32_t mine = tc::smem_u32(red) + 16u * lane;
             float sw4[4], bias4[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                sw4[e] = c4 + e < p.N ? p.s_w[c4 + e] : 0.f;
-                bias4[e] = c4 + e < p.N && p.bias ? p.bias[c4 + e] : 0.f;
+                sw4[e] = c4 + e < end ? p.s_w[c4 + e] : 0.f;
+                bias4[e] = c4 + e < end && p.bias ? p.bias[c4 + e] : 0.f;
             }
             // lane i loads the scale of the warp's i-th token (at most BN / kEpi of them)
             const int j0 = rank + (warp - 2) * S, mine_j = j0 + lane * kEpi * S;
@@ -552,11 +598,11 @@ matmul_few_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constan
                 for (int e = 0; e < 4; ++e) f[e] = fmaf((float)s4[e] * sw4[e], st, bias4[e]);
                 uint16_t* dst = p.out + (long long)(t0 + j) * p.N + c4;
                 if ((p.N & 3) == 0) {                             // 8-byte aligned, and no lane half inside
-                    if (c4 < p.N) *reinterpret_cast<uint2*>(dst) = make_uint2(pack2(f[0], f[1]), pack2(f[2], f[3]));
+                    if (c4 < end) *reinterpret_cast<uint2*>(dst) = make_uint2(pack2(f[0], f[1]), pack2(f[2], f[3]));
                 } else {
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
-                        if (c4 + e < p.N) dst[e] = float_to_bf16_bits(f[e]);
+                        if (c4 + e < end) dst[e] = float_to_bf16_bits(f[e]);
                 }
             }
         }
@@ -565,23 +611,37 @@ matmul_few_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constan
     if (warp == 1) tc::tmem_dealloc(tmem, Ly::COLS);
 }
 
-// Whether each CTA of a call has an SM to itself.  Clusters of more than two leave some SMs of
-// their part of the GPU unused (35 of four with an SM a CTA run in two turns: 5 x 4464 -> 4480
-// 13.0 us, 8.0 with two CTAs an SM).
-bool alone(long long ctas, int S, int sms) { return ctas * 8 <= sms * (S > 2 ? 7LL : 8LL); }
+// CTAs of a call that are resident together with `per` on each SM.  Clusters of more than two
+// leave some SMs of their part of the GPU unused (35 of four with an SM a CTA run in two turns:
+// 5 x 4464 -> 4480 13.0 us, 8.0 with two CTAs an SM).
+long long resident(int S, int per, int sms) { return (long long)per * sms * (S > 2 ? 7 : 8) / 8; }
+
+// Channels of a tile.  Unsplit, as few (from 64 on) as let all CTAs still be resident, on an SM
+// each if those of 128 are, else on two, so that every SM loads its share (8 x 2560 -> 10576 6.9 us
+// with 147 tiles, 7.7 with 83; 8 x 1024 -> 4376 3.7 with 128 channels, 4.0 with 64, 4.6 with 32).
+// Split, more CTAs cost more in clusters and joins than they load sooner (8 x 5120 -> 2560, S = 4:
+// 6.0 with 80 channels or 128; a layer's decode step 25.2, 24.8).
+int tile_rows(int N, int tiles_t, int S, int sms) {
+    if (S > 1) return kRows;
+    const auto ctas = [&](int rows) { return (long long)((N - 1) / rows + 1) * tiles_t; };
+    const long long room = (ctas(kRows) <= sms ? 1LL : 2LL) * sms * 15 / 16;
+    int rows = kRows;
+    while (rows > kLeastRows && ctas(rows - 8) <= room) rows -= 8;
+    return rows;
+}
 
 template <int BN>
 cudaError_t launch(const CUtensorMap& mw, const CUtensorMap& mq, const MatmulArgs& p, int S, cudaStream_t st) {
     using Ly = Layout<BN>;
-    const cudaError_t e =
-        cudaFuncSetAttribute(matmul_few_kernel<BN>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             Ly::smem(Ly::most(kBudgetAlone)));
-    if (e != cudaSuccess) return e;
     const long long ctas = (long long)p.tiles_n * p.tiles_t * S;
-    const int most = Ly::most(alone(ctas, S, device_sm_count()) ? kBudgetAlone : kBudget);
-    const int nk = (p.K - 1) / kBK + 1, slices = (nk - 1) / S + 1;   // a rank's
-    return launch_programmatic(matmul_few_kernel<BN>, (unsigned)ctas, kWarps * 32, Ly::smem(slices < most ? slices : most),
-                               st, S, mw, mq, p, S, slices < most ? slices : most);
+    const int nk = (p.K - 1) / kBK + 1;
+    const int stages = Ly::stages(p.rows, (nk - 1) / S + 1,
+                                  ctas <= resident(S, 1, device_sm_count()) ? kBudgetAlone : kBudget);
+    const cudaError_t e = cudaFuncSetAttribute(matmul_few_kernel<BN>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               1024 + OFF_BUF + kBudgetAlone);
+    if (e != cudaSuccess) return e;
+    return launch_programmatic(matmul_few_kernel<BN>, (unsigned)ctas, kWarps * 32, Ly::smem(p.rows, stages), st, S, mw, mq,
+                               p, S, stages);
 }
 
 }  // namespace few
@@ -596,14 +656,14 @@ bool operand_map(CUtensorMap* m, const int8_t* base, int rows, int K, int box_ro
 // Microseconds that a call on matmul_few_kernel is expected to take, its weights in HBM, with its
 // K axis split S ways: start, end and a tile's rows out; the join (each rank reads (S - 1) / S of
 // a tile's sums from the others, at about 2.4 TB/s over all SMs); and a rank's slices, each
-// (128 + bn) x 128 bytes at 96 bytes a nanosecond into an SM that holds one CTA, 38 for each of
-// two, 1.2 times that with rows that are not whole 32-byte sectors.
-double few_estimate(long long tiles, int nk, int bn, int S, bool sectors, int sms) {
+// (rows + bn) x 128 bytes at 111 bytes a nanosecond into an SM that holds one CTA, 38 for each of
+// two, 1.25 times that with rows that are not whole 32-byte sectors.
+double few_estimate(long long tiles, int rows, int nk, int bn, int S, bool sectors, int sms) {
     const long long ctas = tiles * S;
-    const double slices = (double)nk / S * (few::kRows + bn) * (sectors ? 1.0 : 1.2);
+    const double slices = (double)nk / S * (rows + bn) * (sectors ? 1.0 : 1.25);
     const double fixed = 2.4 + 1.2 * bn / 128 +
-                         (S > 1 ? 0.5 + 0.1 * S + (double)ctas * bn * 512e-6 * (S - 1) / S / 2.4 : 0.0);
-    if (few::alone(ctas, S, sms)) return fixed + slices / 750.0;
+                         (S > 1 ? 0.2 + 0.1 * S + (double)ctas * bn * 512e-6 * (S - 1) / S / 2.4 : 0.0);
+    if (ctas <= few::resident(S, 1, sms)) return fixed + slices / 870.0;
     double turns = (double)ctas / (2 * sms);
     turns = turns <= 1.0 ? 1.0 : 0.5 * (turns + (double)((ctas - 1) / (2 * sms) + 1));
     return fixed + turns * slices / 300.0 + (turns - 1.0) * 4.0;
@@ -622,34 +682,36 @@ double pair_estimate(long long tiles, int nk, bool sectors, bool aligned, int sm
 // expected to take less; the split S that is (all CTAs resident at a time, and none up to 4
 // slices: 31 x 432 -> 593 3.6 us whole, 4.4 and 4.2 split by 2 and 4).  Over 150 other sizes than
 // the estimates were fitted to, drawn at random (1 to 1024 tokens, K to 8192, N to 18560), the
-// choice takes 1.5% longer than the best of all in the geometric mean.  Measured in a graph, each
+// choice takes 1.0% longer than the best of all in the geometric mean.  Measured in a graph, each
 // call's weights in HBM, microseconds with S = 1, 2, 4, 8 and on pairs:
-//    8 x 5120 -> 2560  11.3  7.6  6.2  6.0 15.7      64 x 4096 -> 2048  10.4  7.8  6.3  6.8  13.7
-//    8 x 8192 -> 4096  16.8 10.8  9.4  8.7 23.9     512 x 8192 -> 4096  22.8 20.1 29.7 50.0  23.7
+//    8 x 5120 -> 2560   7.1  6.9  5.6  6.1 15.8      64 x 4096 -> 2048   7.8  7.1  5.5  6.8  13.8
+//    8 x 8192 -> 4096  10.4 10.1  9.0  9.7 23.4     512 x 8192 -> 4096  23.3 20.5 31.0 54.6  23.9
 cudaError_t launch_matmul_i8(int T, int K, int N, const int8_t* q, const float* s_t, const int8_t* Wq,
                              const float* s_w, const float* bias, uint16_t* out, int* status, cudaStream_t st) {
     CUtensorMap mw, mq;
-    MatmulArgs p{T, K, N, 0, 0, s_t, s_w, bias, out, status};
+    MatmulArgs p{T, K, N, 0, 0, s_t, s_w, bias, out, status, 0, Wq};
     const int sms = device_sm_count(), nk = tiles_of(K, kBK);
     const int bn = T <= 16 ? 16 : T <= 32 ? 32 : T <= 64 ? 64 : 128;
-    const long long few_tiles = (long long)tiles_of(N, few::kRows) * tiles_of(T, bn);
+    const int few_t = tiles_of(T, bn);
     const long long pair_tiles = (long long)tiles_of(T, pair::kTile) * tiles_of(N, pair::kTile);
     const bool sectors = K % 32 == 0;
     int S = 1;
-    double few_us = few_estimate(few_tiles, nk, bn, 1, sectors, sms);
-    for (int c : {2, 4, 8}) {
-        if (nk <= 4 || c > nk || few_tiles * c * 4 > 7LL * sms) break;
-        const double us = few_estimate(few_tiles, nk, bn, c, sectors, sms);
-        if (us < few_us) {
+    double few_us = 0.0;
+    for (int c : {1, 2, 4, 8}) {
+        if (c > 1 && (nk <= 4 || c > nk || (long long)tiles_of(N, few::kRows) * few_t * c * 4 > 7LL * sms)) break;
+        const int rows = few::tile_rows(N, few_t, c, sms);
+        const double us = few_estimate((long long)tiles_of(N, rows) * few_t, rows, nk, bn, c, sectors, sms);
+        if (c == 1 || us < few_us) {
             few_us = us;
             S = c;
+            p.rows = rows;
         }
     }
     const double pair_us = pair_estimate(pair_tiles, nk, sectors, N % 8 == 0, sms);
     if (T <= 64 || few_us <= pair_us) {
-        p.tiles_n = tiles_of(N, few::kRows);
-        p.tiles_t = tiles_of(T, bn);
-        if (!operand_map(&mw, Wq, N, K, few::kRows) || !operand_map(&mq, q, T, K, bn)) return cudaErrorInvalidValue;
+        p.tiles_n = tiles_of(N, p.rows);
+        p.tiles_t = few_t;
+        if (!operand_map(&mw, Wq, N, K, p.rows) || !operand_map(&mq, q, T, K, bn)) return cudaErrorInvalidValue;
         if (bn == 16) return few::launch<16>(mw, mq, p, S, st);
         if (bn == 32) return few::launch<32>(mw, mq, p, S, st);
         if (bn == 64) return few::launch<64>(mw, mq, p, S, st);
