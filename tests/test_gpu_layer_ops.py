@@ -210,6 +210,29 @@ def test_matmul(torch_cuda, T, K, N, biased):
     assert (off <= lim).all(), (off / lim).max()
 
 
+def test_matmul_every_kernel_and_split_gives_the_same_bits(torch_cuda):
+    """Sizes over the choices (tile heights, CTAs an SM, K splits, ragged ends): the exact sum, two fp32 products and
+    one rounding, bit for bit."""
+    torch = torch_cuda
+    import int8_quant_b200 as iq
+    import random
+    rng = random.Random(5)
+    sizes = [(1, 8192, 9400), (20, 4096, 8500), (64, 8192, 18000), (3, 2064, 20000), (40, 3088, 21000), (9, 4464, 4480),
+             (17, 5360, 2137), (5, 144, 3000), (50, 272, 9000), (64, 400, 64), (16, 4000, 2040), (100, 2928, 8647)]
+    for _ in range(80):
+        sizes.append((round(1500 ** rng.random()), 16 * round(400 ** rng.random()), round(20000 ** rng.random())))
+    g, st = _gen(torch, 1), torch.zeros(1, dtype=torch.int32, device="cuda")
+    for T, K, N in sizes:
+        q = torch.randint(-128, 128, (T, K), generator=g, device="cuda", dtype=torch.int8)
+        Wq = torch.randint(-128, 128, (N, K), generator=g, device="cuda", dtype=torch.int8)
+        s_t, s_w = torch.rand(T, generator=g, device="cuda"), torch.rand(N, generator=g, device="cuda") * 1e-3
+        out = torch.full((T, N), float("nan"), device="cuda").bfloat16()
+        iq.ssd_matmul_i8(q, s_t, Wq, s_w, None, out, st)
+        acc = (q.double() @ Wq.double().T).float()                       # exact below 2^53, rounded once
+        assert torch.equal(out, (acc * s_w * s_t[:, None]).bfloat16()), (T, K, N)
+    assert iq.ssd_workspace_status(st) == 0
+
+
 @pytest.mark.parametrize("code", [127, -128])
 def test_matmul_extreme_sums_stay_exact(torch_cuda, code):
     """All codes the largest over the longest k: the sum 131056 * 128^2 fits INT32, the next k's would not."""
