@@ -453,8 +453,10 @@ matmul_few_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constan
     if (warp == 1) {
         tc::tmem_alloc(tmem_slot, Ly::COLS);
         tc::tmem_relinquish();
+        // not before: a CTA of the next kernel that took the columns this one still needs would
+        // wait for this kernel's end with them
+        grid_release();
     }
-    grid_release();
     grid_wait();
     tc::tc_fence_before();
     __syncthreads();
