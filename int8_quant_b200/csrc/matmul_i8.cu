@@ -374,10 +374,12 @@ constexpr int kMaxStages = 16, kLeastRows = 64;
 // 17.2, 15.3; 64 x 5120 -> 2560 7.0 with 768, 6.6 with all its 1280).
 constexpr int kAhead = 1280;
 constexpr int kLoader2 = 3;                           // the second loading warp, until its epilogue
-// Shared memory for stages where two CTAs share an SM, and where none has to: the bytes on
-// their way bound an SM's rate (8 x 4096 -> 18560 from HBM 14.5 us with 96 KB, 13.7 with 148;
-// 64 x 4096 -> 2048 6.6, 5.8).  148 KB leave room for the CTAs of the next kernel.
-constexpr int kBudget = 98304, kBudgetAlone = 151552;
+// Shared memory for stages where two CTAs share an SM, and where none has to: the bytes on their
+// way bound an SM's rate (8 x 5120 -> 2560 7.5 us with 96 KB, 5.7 with 148, 5.6 with 208; 256 x 8192
+// -> 4096 16.0 with 148, 14.7 with 208).  For few tokens 148 KB leave room for the next kernels'
+// CTAs (a decode step of batch 1 21.55 us, 21.63 with 208).
+constexpr int kBudget = 98304;
+constexpr int alone_budget(int bn) { return bn < 64 ? 151552 : 212992; }
 constexpr int B_FULL = 0, B_EMPTY = kMaxStages, B_DONE = 2 * kMaxStages, NBAR = B_DONE + 1;
 constexpr int OFF_FLAG = NBAR * 8, OFF_TMEM = OFF_FLAG + 8, OFF_BUF = 1024;
 static_assert(OFF_TMEM + 8 <= OFF_BUF, "barriers in front of the stages");
@@ -638,9 +640,9 @@ cudaError_t launch(const CUtensorMap& mw, const CUtensorMap& mq, const MatmulArg
     const long long ctas = (long long)p.tiles_n * p.tiles_t * S;
     const int nk = (p.K - 1) / kBK + 1;
     const int stages = Ly::stages(p.rows, (nk - 1) / S + 1,
-                                  ctas <= resident(S, 1, device_sm_count()) ? kBudgetAlone : kBudget);
+                                  ctas <= resident(S, 1, device_sm_count()) ? alone_budget(BN) : kBudget);
     const cudaError_t e = cudaFuncSetAttribute(matmul_few_kernel<BN>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               1024 + OFF_BUF + kBudgetAlone);
+                                               1024 + OFF_BUF + alone_budget(BN));
     if (e != cudaSuccess) return e;
     return launch_programmatic(matmul_few_kernel<BN>, (unsigned)ctas, kWarps * 32, Ly::smem(p.rows, stages), st, S, mw, mq,
                                p, S, stages);
