@@ -410,11 +410,12 @@ struct Layout {
 // Cluster rank r takes the K slices [r nk / S, (r + 1) nk / S) of the tile (channels n0 ..,
 // tokens t0 ..), keeps its partial sums in shared memory, and then finishes the tokens
 // r, r + S, ... of the tile with every rank's partial sums.
-template <int BN>
+template <int BN, bool SPLIT>
 __global__ void __launch_bounds__(kWarps * 32)
 matmul_few_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_q,
-                  const __grid_constant__ MatmulArgs p, int S, int stages) {
+                  const __grid_constant__ MatmulArgs p, int split, int stages) {
     using Ly = Layout<BN>;
+    const int S = SPLIT ? split : 1;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* sm = smem_raw + ((1024u - (tc::smem_u32(smem_raw) & 1023u)) & 1023u);
     uint64_t* bar = reinterpret_cast<uint64_t*>(sm);
@@ -422,7 +423,7 @@ matmul_few_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constan
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + OFF_TMEM);
     uint8_t* buf = sm + OFF_BUF;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int rank = S > 1 ? (int)tc::cluster_rank() : 0;
+    const int rank = SPLIT ? (int)tc::cluster_rank() : 0;
     const int tile = blockIdx.x / S;
     const int n0 = (tile % p.tiles_n) * p.rows, t0 = (tile / p.tiles_n) * BN;
     const int stage = Ly::stage(p.rows);
@@ -464,6 +465,22 @@ matmul_few_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constan
     __syncthreads();
     tc::tc_fence_after();
     const uint32_t tmem = *tmem_slot;
+
+    // The epilogue's factors, asked for ahead of everything that it waits for (8 x 5120 -> 2560
+    // 5.7 us without, 5.4 so; with the split at run time 64 x 2560 -> 10576 7.9 us, 7.1 so).  Unsplit, a thread has a channel, and lane i the scale of the token
+    // 16 part + i % 16; split, a lane has four channels, and lane i the scale of its warp's i-th token
+    // (at most BN / kEpi).
+    const int quarter = warp & 3, row = quarter * 32 + lane, ch = n0 + row, part = (warp - 2) / 4;
+    const int c4 = SPLIT ? n0 + 4 * lane : ch, end = min(p.N, n0 + p.rows), live = min(BN, p.T - t0);
+    const int j0 = rank + (warp - 2) * S, token = SPLIT ? j0 + lane * kEpi * S : 16 * part + (lane & 15);
+    float sw[4], bias[4], scale = 0.f;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const bool in = warp >= 2 && c4 + e < end && (e == 0 || SPLIT);
+        sw[e] = in ? p.s_w[c4 + e] : 0.f;
+        bias[e] = in && p.bias ? p.bias[c4 + e] : 0.f;
+    }
+    if ((SPLIT || BN <= 32) && warp >= 2 && token < live) scale = p.s_t[t0 + token];
 
     bool ok = true;
     if (warp == 0 || warp == kLoader2) {
@@ -523,11 +540,7 @@ matmul_few_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constan
         else tc::mbar_wait(bar + B_DONE, 0, kDrainLimit);
         __syncwarp();
     }
-    const int quarter = warp & 3, row = quarter * 32 + lane, ch = n0 + row, part = (warp - 2) / 4;
-    const bool in = warp >= 2 && row < p.rows && ch < p.N;
-    const float sw = in ? p.s_w[ch] : 0.f;
-    const float bias = in && p.bias ? p.bias[ch] : 0.f;
-    const int live = min(BN, p.T - t0);
+    const bool in = warp >= 2 && ch < end;
     int* red = reinterpret_cast<int*>(buf);
     // the other warps wait here, not at the MMA's barrier: eight of them asking it slow every
     // barrier of the CTA down
@@ -550,18 +563,18 @@ matmul_few_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constan
 #pragma unroll
                     for (int j = 0; j < 16; ++j) v[j] += v1[j];
                 }
-                if (S > 1) {
+                if (SPLIT) {
 #pragma unroll
                     for (int j = 0; j < 16; ++j) red[(c + j) * kRows + row] = (int)v[j];
                 } else {
-                    const int mine = c + (lane & 15);             // this lane's token, for its scale
-                    const float scale = mine < live ? p.s_t[t0 + mine] : 0.f;
+                    const int mine = c + (lane & 15);
+                    const float now = BN <= 32 ? scale : mine < live ? p.s_t[t0 + mine] : 0.f;
 #pragma unroll
                     for (int j = 0; j < 16; ++j) {
-                        const float st = __shfl_sync(0xffffffffu, scale, j);
+                        const float st = __shfl_sync(0xffffffffu, now, j);
                         if (in && c + j < live)
                             dst[(long long)(c + j) * p.N] =
-                                float_to_bf16_bits(fmaf((float)(int)v[j] * sw, st, bias));
+                                float_to_bf16_bits(fmaf((float)(int)v[j] * sw[0], st, bias[0]));
                     }
                 }
             }
@@ -569,21 +582,11 @@ matmul_few_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constan
     }
     tc::tc_fence_before();
     __syncthreads();
-    if (S > 1) {
+    if (SPLIT) {
         tc::cluster_sync();
         if (warp >= 2 && ok) {
             // a warp takes a token of this rank's share, a lane four channels
-            const int c4 = n0 + 4 * lane, end = min(p.N, n0 + p.rows);
             const uint32_t mine = tc::smem_u32(red) + 16u * lane;
-            float sw4[4], bias4[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                sw4[e] = c4 + e < end ? p.s_w[c4 + e] : 0.f;
-                bias4[e] = c4 + e < end && p.bias ? p.bias[c4 + e] : 0.f;
-            }
-            // lane i loads the scale of the warp's i-th token (at most BN / kEpi of them)
-            const int j0 = rank + (warp - 2) * S, mine_j = j0 + lane * kEpi * S;
-            const float scale = mine_j < live ? p.s_t[t0 + mine_j] : 0.f;
 #pragma unroll 4
             for (int j = j0, i = 0; j < live; j += kEpi * S, ++i) {
                 const float st = __shfl_sync(0xffffffffu, scale, i);
@@ -599,7 +602,7 @@ matmul_few_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constan
                 const int s4[4] = {sum.x, sum.y, sum.z, sum.w};
                 float f[4];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) f[e] = fmaf((float)s4[e] * sw4[e], st, bias4[e]);
+                for (int e = 0; e < 4; ++e) f[e] = fmaf((float)s4[e] * sw[e], st, bias[e]);
                 uint16_t* dst = p.out + (long long)(t0 + j) * p.N + c4;
                 if ((p.N & 3) == 0) {                             // 8-byte aligned, and no lane half inside
                     if (c4 < end) *reinterpret_cast<uint2*>(dst) = make_uint2(pack2(f[0], f[1]), pack2(f[2], f[3]));
@@ -622,7 +625,7 @@ long long resident(int S, int per, int sms) { return (long long)per * sms * (S >
 
 // Channels of a tile.  Unsplit, as few (from 64 on) as let all CTAs still be resident, on an SM
 // each if those of 128 are, else on two, so that every SM loads its share (8 x 2560 -> 10576 6.9 us
-// with 147 tiles, 7.7 with 83; 8 x 1024 -> 4376 3.7 with 128 channels, 4.0 with 64, 4.6 with 32).
+// with 133 tiles, 7.7 with 83; 8 x 1024 -> 4376 3.7 with 128 channels, 4.0 with 64, 4.6 with 32).
 // Split, more CTAs cost more in clusters and joins than they load sooner (8 x 5120 -> 2560, S = 4:
 // 6.0 with 80 channels or 128; a layer's decode step 25.2, 24.8).
 int tile_rows(int N, int tiles_t, int S, int sms) {
@@ -641,10 +644,11 @@ cudaError_t launch(const CUtensorMap& mw, const CUtensorMap& mq, const MatmulArg
     const int nk = (p.K - 1) / kBK + 1;
     const int stages = Ly::stages(p.rows, (nk - 1) / S + 1,
                                   ctas <= resident(S, 1, device_sm_count()) ? alone_budget(BN) : kBudget);
-    const cudaError_t e = cudaFuncSetAttribute(matmul_few_kernel<BN>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    const auto kernel = S > 1 ? matmul_few_kernel<BN, true> : matmul_few_kernel<BN, false>;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                1024 + OFF_BUF + alone_budget(BN));
     if (e != cudaSuccess) return e;
-    return launch_programmatic(matmul_few_kernel<BN>, (unsigned)ctas, kWarps * 32, Ly::smem(p.rows, stages), st, S, mw, mq,
+    return launch_programmatic(kernel, (unsigned)ctas, kWarps * 32, Ly::smem(p.rows, stages), st, S, mw, mq,
                                p, S, stages);
 }
 
