@@ -613,7 +613,8 @@ matmul_few_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constan
                 }
             }
         }
-        tc::cluster_sync();                                       // the others have read this CTA's sums
+        // the others have read this CTA's sums; its stores need not be through (4 to 6% of a split call)
+        tc::cluster_done();
     }
     if (warp == 1) tc::tmem_dealloc(tmem, Ly::COLS);
 }

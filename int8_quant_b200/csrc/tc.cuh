@@ -291,6 +291,12 @@ __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release;" ::: "memory");
     asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
 }
+// Waits until every thread of the cluster is here, without waiting for its stores: reads whose
+// values were used are over.
+__device__ __forceinline__ void cluster_done() {
+    asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory");
+    asm volatile("barrier.cluster.wait;" ::: "memory");
+}
 // (Ordered after a cluster_sync in front of it, but not with this thread's own stores.)
 __device__ __forceinline__ int4 ld_cluster_s32x4(uint32_t addr) {
     int4 v;
