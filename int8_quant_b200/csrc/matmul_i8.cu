@@ -688,13 +688,12 @@ double pair_estimate(long long tiles, int nk, bool sectors, bool aligned, int sm
 }  // namespace
 
 // Which kernel, and how many ranks: matmul_few_kernel up to 64 tokens, else the one that is
-// expected to take less; the split S that is (all CTAs resident at a time, and none up to 4
-// slices: 31 x 432 -> 593 3.6 us whole, 4.4 and 4.2 split by 2 and 4).  Over 150 other sizes than
-// the estimates were fitted to, drawn at random (1 to 1024 tokens, K to 8192, N to 18560), the
-// choice takes 1.0% longer than the best of all in the geometric mean.  Measured in a graph, each
-// call's weights in HBM, microseconds with S = 1, 2, 4, 8 and on pairs:
-//    8 x 5120 -> 2560   7.1  6.9  5.6  6.1 15.8      64 x 4096 -> 2048   7.8  7.1  5.5  6.8  13.8
-//    8 x 8192 -> 4096  10.4 10.1  9.0  9.7 23.4     512 x 8192 -> 4096  23.3 20.5 31.0 54.6  23.9
+// expected to take less; the split S that is (all CTAs resident at a time).  Over 308 sizes, most
+// drawn at random (1 to 1024 tokens, K to 8192, N to 18560), the choice takes 1.2% longer than the
+// best of all in the geometric mean.  Measured in a graph, each call's weights in HBM,
+// microseconds with S = 1, 2, 4, 8 and on pairs:
+//    8 x 5120 -> 2560   6.8  6.5  5.1  5.3 15.7      64 x 4096 -> 2048   6.8  6.9  5.2  6.6  13.7
+//    8 x 8192 -> 4096   9.9  9.5  8.3  8.8 24.0     512 x 8192 -> 4096  19.2 19.5 28.7 46.5  23.5
 cudaError_t launch_matmul_i8(int T, int K, int N, const int8_t* q, const float* s_t, const int8_t* Wq,
                              const float* s_w, const float* bias, uint16_t* out, int* status, cudaStream_t st) {
     CUtensorMap mw, mq;
@@ -707,7 +706,7 @@ cudaError_t launch_matmul_i8(int T, int K, int N, const int8_t* q, const float* 
     int S = 1;
     double few_us = 0.0;
     for (int c : {1, 2, 4, 8}) {
-        if (c > 1 && (nk <= 4 || c > nk || (long long)tiles_of(N, few::kRows) * few_t * c * 4 > 7LL * sms)) break;
+        if (c > 1 && (c > nk || (long long)tiles_of(N, few::kRows) * few_t * c * 4 > 7LL * sms)) break;
         const int rows = few::tile_rows(N, few_t, c, sms);
         const double us = few_estimate((long long)tiles_of(N, rows) * few_t, rows, nk, bn, c, sectors, sms);
         if (c == 1 || us < few_us) {
