@@ -294,6 +294,7 @@ class SsdLayer:
         if self.E % 8 or self.E < self.hp + self.ch + self.H:
             raise ValueError("in_proj's rows: at least 2*H*P + 2*G*N + H of them, and a multiple of 8")
         self.dev = weights["in_q"].device
+        self.index = weights["in_q"].get_device()
         self.params = None
         if path == "w8a8":
             self.params = ssd.i8_params(scales["s_B"], scales["s_C"], scales["s_x"], scales["s_s"], shift)
@@ -319,6 +320,9 @@ class SsdLayer:
         Returns (the layer's output [b, L, d] bf16, the residual to hand on, the state after each row's last
         token).  Outputs behind a row's last token mean nothing.  Buffers are torch's, on its current stream:
         with `stream` given, make that the current one too."""
+        if torch.cuda.current_device() != self.index:    # the scan launches on the current device
+            with torch.cuda.device(self.index):
+                return self.prefill(hidden, residual, state, lengths, stream)
         b, L, d = hidden.shape
         T, w, new = b * L, self.w, self.new
         q, s = new(T, d, dtype=torch.int8), new(T, dtype=torch.float32)
@@ -376,6 +380,9 @@ class SsdLayerDecoder:
         """hidden [b, d] bf16, residual [b, d] fp32 or bf16, or None (the stream starts here, in fp32).  Returns
         (output [b, d] bf16, the residual to hand on)."""
         l, w = self.layer, self.layer.w
+        if torch.cuda.current_device() != l.index:       # the scan's step launches on the current device
+            with torch.cuda.device(l.index):
+                return self.step(hidden, residual, stream)
         res = self.res[torch.float32 if residual is None else residual.dtype]
         ssd.ssd_add_rmsnorm_i8(hidden, residual, w["norm"], l.eps, res, self.q, self.s, stream=stream)
         ssd.ssd_matmul_i8(self.q, self.s, w["in_q"], w["in_s"], None, self.rows, l.status, stream)

@@ -1,0 +1,75 @@
+"""SsdLayer's and its decoder's host side (no GPU): where their calls go, with the library's functions replaced by
+recorders and torch's current device and stream by fakes."""
+import contextlib
+
+import pytest
+
+torch = pytest.importorskip("torch")
+
+from int8_quant_b200 import runner, ssd  # noqa: E402
+
+H, P, G, N, D, W = 2, 16, 1, 16, 32, 4
+HP, CH = H * P, H * P + 2 * G * N
+CALLS = ("ssd_add_rmsnorm_i8", "ssd_matmul_i8", "ssd_conv_fwd_bf16", "ssd_conv_step_bf16", "ssd_gated_rmsnorm_i8",
+         "ssd_quantize_inputs", "ssd_scan_fwd_bf16_from_state", "ssd_scan_fwd_i8_from_state", "ssd_decode_step_bf16",
+         "ssd_decode_step_i8")
+
+
+def make_weights():
+    E = HP + CH + 8
+    return {"norm": torch.ones(D), "gate_norm": torch.ones(HP), "in_q": torch.zeros(E, D, dtype=torch.int8),
+            "in_s": torch.ones(E), "out_q": torch.zeros(D, HP, dtype=torch.int8), "out_s": torch.ones(D),
+            "conv_w": torch.zeros(W, CH), "dt_bias": torch.zeros(H), "A": -torch.ones(H), "D": torch.ones(H)}
+
+
+def make_scales():
+    return {"s_B": torch.ones(G), "s_C": torch.ones(G), "s_x": torch.ones(HP), "s_s": torch.ones(HP)}
+
+
+def make_layer(path):
+    return runner.SsdLayer(make_weights(), (H, P, G, N), path, 64, make_scales() if path == "w8a8" else None)
+
+
+class World:
+    """A current device and stream, and the calls made under them."""
+
+    def __init__(self, monkeypatch):
+        self.device, self.stream, self.calls = 0, "device 0's", []
+
+        @contextlib.contextmanager
+        def device(index):
+            was, self.device, self.stream = (self.device, self.stream), index, f"device {index}'s"
+            yield
+            self.device, self.stream = was
+
+        @contextlib.contextmanager
+        def stream(s):
+            was, self.stream = self.stream, s.cuda_stream
+            yield
+            self.stream = was
+
+        monkeypatch.setattr(torch.cuda, "current_device", lambda: self.device)
+        monkeypatch.setattr(torch.cuda, "device", device)
+        monkeypatch.setattr(torch.cuda, "stream", stream)
+        for name in CALLS:
+            monkeypatch.setattr(ssd, name, lambda *a, _n=name, **k: self.calls.append((_n, self.device, self.stream)))
+
+
+@pytest.fixture
+def world(monkeypatch):
+    return World(monkeypatch)
+
+
+@pytest.mark.parametrize("path", ["bf16", "w8a8"])
+@pytest.mark.parametrize("current", [0, 1])
+def test_every_call_runs_on_the_layers_device(world, path, current):
+    """The scan and its step launch on the current device: a layer on another one makes its own the current one, and
+    leaves the caller's as it was."""
+    layer = make_layer(path)
+    layer.index = 1
+    world.device, world.stream = current, f"device {current}'s"
+    layer.prefill(torch.zeros(1, 3, D, dtype=torch.bfloat16))
+    assert len(world.calls) == (7 if path == "w8a8" else 6)
+    layer.decoder(layer.zero_state(1)).step(torch.zeros(1, D, dtype=torch.bfloat16))
+    assert {c[1:] for c in world.calls} == {(1, "device 1's")}
+    assert (world.device, world.stream) == (current, f"device {current}'s")
