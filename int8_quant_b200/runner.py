@@ -5,6 +5,8 @@ into libssd.so.
 """
 from __future__ import annotations
 
+import contextlib
+
 import numpy as np
 import torch
 
@@ -318,40 +320,54 @@ class SsdLayer:
         """hidden [b, L, d] bf16; residual [b, L, d] fp32 or bf16, or None (the stream starts here, in fp32); state:
         what an earlier call returned (None: zeros); lengths [b] int32: the tokens of each row of a padded batch.
         Returns (the layer's output [b, L, d] bf16, the residual to hand on, the state after each row's last
-        token).  Outputs behind a row's last token mean nothing.  Buffers are torch's, on its current stream:
-        with `stream` given, make that the current one too."""
-        if torch.cuda.current_device() != self.index:    # the scan launches on the current device
-            with torch.cuda.device(self.index):
-                return self.prefill(hidden, residual, state, lengths, stream)
+        token).  Outputs behind a row's last token mean nothing.  Runs on the layer's device, and there on `stream` (a
+        torch stream or a handle; None: the current one), to which the buffers and outputs belong as well."""
+        with self._on(stream):
+            return self._prefill(hidden, residual, state, lengths)
+
+    @contextlib.contextmanager
+    def _on(self, stream=None):
+        """The layer's device and `stream` as the current ones.  The scan launches on the current device, and torch
+        hands memory that one call gave back to the next call of the same stream."""
+        with contextlib.ExitStack() as made:
+            if torch.cuda.current_device() != self.index:
+                made.enter_context(torch.cuda.device(self.index))
+            if stream is not None:
+                if not hasattr(stream, "cuda_stream"):
+                    stream = torch.cuda.ExternalStream(int(stream), device=self.dev) if int(stream) else \
+                        torch.cuda.default_stream(self.dev)
+                made.enter_context(torch.cuda.stream(stream))
+            yield
+
+    def _prefill(self, hidden, residual, state, lengths):
         b, L, d = hidden.shape
         T, w, new = b * L, self.w, self.new
         q, s = new(T, d, dtype=torch.int8), new(T, dtype=torch.float32)
         res = None if residual is None else residual.reshape(T, d)
         res_out = new(T, d, dtype=torch.float32 if res is None else res.dtype)
-        ssd.ssd_add_rmsnorm_i8(hidden.reshape(T, d), res, w["norm"], self.eps, res_out, q, s, stream=stream)
+        ssd.ssd_add_rmsnorm_i8(hidden.reshape(T, d), res, w["norm"], self.eps, res_out, q, s)
         rows = new(b, L, self.E)
-        ssd.ssd_matmul_i8(q, s, w["in_q"], w["in_s"], None, rows.view(T, self.E), self.status, stream)
+        ssd.ssd_matmul_i8(q, s, w["in_q"], w["in_s"], None, rows.view(T, self.E), self.status)
         _, xbc, dt_raw = self.slices(rows)
         x, B, C = new(b, L, self.H, self.P), new(b, L, self.G, self.N), new(b, L, self.G, self.N)
         dt, conv = new(b, L, self.H, dtype=torch.float32), new(b, self.width - 1, self.ch)
         ssd.ssd_conv_fwd_bf16(xbc, dt_raw, w["conv_w"], w.get("conv_b"), w["dt_bias"], lengths,
-                              None if state is None else state["conv"], x, dt, B, C, conv, stream)
+                              None if state is None else state["conv"], x, dt, B, C, conv)
         y = new(b, L, self.H, self.P)
         init = None if state is None else state["ssd"]
         shape = ssd.SsdShape.of(b, L, self.H, self.P, self.G, self.N, self.chunk)
         ws = new(max(ssd.ssd_workspace_bytes(shape, self.path == "w8a8"), 256), dtype=torch.uint8)
         if self.path == "bf16":
             fin = new(b, self.H, self.P, self.N, dtype=torch.float32)
-            ssd.ssd_scan_fwd_bf16_from_state(shape, x, dt, w["A"], B, C, w["D"], init, y, fin, ws, stream)
+            ssd.ssd_scan_fwd_bf16_from_state(shape, x, dt, w["A"], B, C, w["D"], init, y, fin, ws)
         else:
             fin = new(b, self.H, self.P, self.N, dtype=torch.int8)
             Bq, Cq = new(*B.shape, dtype=torch.int8), new(*C.shape, dtype=torch.int8)
-            ssd.ssd_quantize_inputs(shape, B, C, self.scales["s_B"], self.scales["s_C"], Bq, Cq, stream)
-            ssd.ssd_scan_fwd_i8_from_state(shape, x, dt, w["A"], Bq, Cq, w["D"], self.params, init, y, fin, ws, stream)
+            ssd.ssd_quantize_inputs(shape, B, C, self.scales["s_B"], self.scales["s_C"], Bq, Cq)
+            ssd.ssd_scan_fwd_i8_from_state(shape, x, dt, w["A"], Bq, Cq, w["D"], self.params, init, y, fin, ws)
         qg, out = new(T, self.hp, dtype=torch.int8), new(b, L, d)
-        ssd.ssd_gated_rmsnorm_i8(y.view(T, self.hp), rows.view(T, self.E)[:, :self.hp], w["gate_norm"], self.eps, qg, s,
-                                 stream=stream)
-        ssd.ssd_matmul_i8(qg, s, w["out_q"], w["out_s"], w.get("out_corr"), out.view(T, d), self.status, stream)
+        ssd.ssd_gated_rmsnorm_i8(y.view(T, self.hp), rows.view(T, self.E)[:, :self.hp], w["gate_norm"], self.eps, qg, s)
+        ssd.ssd_matmul_i8(qg, s, w["out_q"], w["out_s"], w.get("out_corr"), out.view(T, d), self.status)
         return out, res_out.view(b, L, d), {"conv": conv, "ssd": fin}
 
     def decoder(self, state: dict) -> "SsdLayerDecoder":
@@ -378,7 +394,7 @@ class SsdLayerDecoder:
 
     def step(self, hidden, residual=None, stream=None):
         """hidden [b, d] bf16, residual [b, d] fp32 or bf16, or None (the stream starts here, in fp32).  Returns
-        (output [b, d] bf16, the residual to hand on)."""
+        (output [b, d] bf16, the residual to hand on).  stream: as in SsdLayer.prefill."""
         l, w = self.layer, self.layer.w
         if torch.cuda.current_device() != l.index:       # the scan's step launches on the current device
             with torch.cuda.device(l.index):

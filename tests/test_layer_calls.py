@@ -73,3 +73,20 @@ def test_every_call_runs_on_the_layers_device(world, path, current):
     layer.decoder(layer.zero_state(1)).step(torch.zeros(1, D, dtype=torch.bfloat16))
     assert {c[1:] for c in world.calls} == {(1, "device 1's")}
     assert (world.device, world.stream) == (current, f"device {current}'s")
+
+
+@pytest.mark.parametrize("path", ["bf16", "w8a8"])
+def test_a_prompts_buffers_belong_to_its_stream(world, path):
+    """With a stream given, the calls and the allocations around them are that stream's: memory that a call gives back
+    is used again in the order of the stream it was used on."""
+    class Side:
+        cuda_stream = "side"
+
+    layer = make_layer(path)
+    layer.index = 0
+    made = []
+    new = layer.new
+    layer.new = lambda *a, **k: made.append(world.stream) or new(*a, **k)
+    layer.prefill(torch.zeros(1, 3, D, dtype=torch.bfloat16), stream=Side())
+    assert set(made) == {"side"} and {c[2] for c in world.calls} == {"side"}
+    assert world.stream == "device 0's"
