@@ -300,7 +300,18 @@ class SsdLayer:
         self.params = None
         if path == "w8a8":
             self.params = ssd.i8_params(scales["s_B"], scales["s_C"], scales["s_x"], scales["s_s"], shift)
+        # the error word of the products, and of the scans once they are done
         self.status = torch.zeros(1, dtype=torch.int32, device=self.dev)
+        self._word0 = torch.zeros(1, dtype=torch.int64, device=self.dev)
+
+    def check(self, stream=None):
+        """Waits for `stream` (None: the current one) and raises SsdError if a device-side wait of this layer or its
+        decoders expired since the last check (SSD_ERR_TIMEOUT): outputs and states since then are not to be used.
+        Nothing else raises that error, since calls return before their kernels run."""
+        with self._on(stream):
+            bad = ssd.ssd_workspace_status(self.status)
+        if bad:
+            raise ssd.SsdError("SsdLayer", bad)
 
     def new(self, *shape, dtype=torch.bfloat16):
         return torch.empty(shape, dtype=dtype, device=self.dev)
@@ -366,6 +377,9 @@ class SsdLayer:
             ssd.ssd_quantize_inputs(shape, B, C, self.scales["s_B"], self.scales["s_C"], Bq, Cq)
             ssd.ssd_scan_fwd_i8_from_state(shape, x, dt, w["A"], Bq, Cq, w["D"], self.params, init, y, fin, ws)
         qg, out = new(T, self.hp, dtype=torch.int8), new(b, L, d)
+        if b > 0:
+            # the scan's error word ends with its workspace; an atomic maximum, as other streams' calls may do the same
+            self.status.scatter_reduce_(0, self._word0, ws[:4].view(torch.int32), "amax")
         ssd.ssd_gated_rmsnorm_i8(y.view(T, self.hp), rows.view(T, self.E)[:, :self.hp], w["gate_norm"], self.eps, qg, s)
         ssd.ssd_matmul_i8(qg, s, w["out_q"], w["out_s"], w.get("out_corr"), out.view(T, d), self.status)
         return out, res_out.view(b, L, d), {"conv": conv, "ssd": fin}

@@ -35,3 +35,59 @@ def test_prefill_on_a_stream_that_is_not_the_current_one(torch_cuda, path):
         waste = [torch.full((1 << n,), 1.0, device="cuda") for n in range(8, 22)]
         torch.cuda.synchronize()
         assert _same(got, ref) and len(waste) == 14
+
+
+@pytest.mark.parametrize("path", ["bf16", "w8a8"])
+def test_check_raises_an_expired_wait(torch_cuda, monkeypatch, path):
+    """The word that an expired wait leaves in the scan's workspace, or in the products' status, written here from the
+    host's side after a call that succeeded."""
+    torch = torch_cuda
+    import int8_quant_b200 as iq
+    layer = _layer(torch, path)
+    hidden = _hidden(torch, 8, 2, 40, D)
+    name = "ssd_scan_fwd_bf16_from_state" if path == "bf16" else "ssd_scan_fwd_i8_from_state"
+    scan, words = getattr(iq.ssd, name), []
+
+    def call(*a):
+        scan(*a)
+        if words:
+            a[-1][:4].view(torch.int32).fill_(words.pop())
+
+    monkeypatch.setattr(iq.ssd, name, call)
+    layer.prefill(hidden)
+    layer.check()
+    words.append(5)
+    ref = layer.prefill(hidden)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    torch.use_deterministic_algorithms(True)
+    try:
+        got = layer.prefill(hidden, stream=side)
+    finally:
+        torch.use_deterministic_algorithms(False)
+    with pytest.raises(iq.SsdError) as err:
+        layer.check(side)
+    assert err.value.status == 5 and _same(got, ref)
+    layer.check()
+    layer.status.fill_(5)
+    with pytest.raises(iq.SsdError):
+        layer.check()
+    layer.check()
+    layer.prefill(hidden[:0])                          # no rows: no scan, and no word of one
+    layer.prefill(hidden[:, :0])
+    layer.check()
+
+
+def test_status_is_kept_by_a_captured_prompt(torch_cuda):
+    torch = torch_cuda
+    layer = _layer(torch, "w8a8")
+    hidden = _hidden(torch, 8, 2, 40, D)
+    ref = layer.prefill(hidden)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        got = layer.prefill(hidden)
+    for _ in range(2):
+        g.replay()
+        layer.check()
+        assert _same(got, ref)

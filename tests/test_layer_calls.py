@@ -90,3 +90,29 @@ def test_a_prompts_buffers_belong_to_its_stream(world, path):
     layer.prefill(torch.zeros(1, 3, D, dtype=torch.bfloat16), stream=Side())
     assert set(made) == {"side"} and {c[2] for c in world.calls} == {"side"}
     assert world.stream == "device 0's"
+
+
+@pytest.mark.parametrize("path", ["bf16", "w8a8"])
+def test_an_expired_wait_of_the_scan_outlives_its_workspace(world, monkeypatch, path):
+    """The scan's error word lies in a workspace that ends with the call: check() raises it, also after later calls
+    without an error, and then is clear again."""
+    layer = make_layer(path)
+    words = iter([0, 5, 0])
+    scan = "ssd_scan_fwd_bf16_from_state" if path == "bf16" else "ssd_scan_fwd_i8_from_state"
+    monkeypatch.setattr(ssd, scan, lambda *a: a[-1][:4].view(torch.int32).fill_(next(words)))
+
+    def status(word, stream=None):
+        bad = int(word)
+        word.zero_()
+        return bad
+
+    monkeypatch.setattr(ssd, "ssd_workspace_status", status)
+    hidden = torch.zeros(1, 3, D, dtype=torch.bfloat16)
+    layer.prefill(hidden)
+    layer.check()
+    layer.prefill(hidden)
+    layer.prefill(hidden)
+    with pytest.raises(ssd.SsdError) as err:
+        layer.check()
+    assert err.value.status == 5
+    layer.check()
