@@ -298,6 +298,14 @@ class SsdLayer:
         self.dev = weights["in_q"].device
         self.index = weights["in_q"].get_device()
         self.params = None
+        # what the scan is given by address alone; the other weights are checked by their calls
+        addressed = [("A", weights["A"], self.H), ("D", weights["D"], self.H)]
+        if path == "w8a8":
+            addressed += [(k, scales[k], n) for k, n in (("s_B", self.G), ("s_C", self.G), ("s_x", self.hp),
+                                                         ("s_s", self.hp))]
+        for name, t, n in addressed:
+            if not self._is(t, torch.float32, (n,)):
+                raise ValueError(f"{name} has to be a contiguous float32 tensor [{n}] on {self.dev}")
         if path == "w8a8":
             self.params = ssd.i8_params(scales["s_B"], scales["s_C"], scales["s_x"], scales["s_s"], shift)
         # the error word of the products, and of the scans once they are done
@@ -320,6 +328,18 @@ class SsdLayer:
         """z, xBC and dt of in_proj's output rows."""
         hp, ch = self.hp, self.ch
         return rows[..., :hp], rows[..., hp:hp + ch], rows[..., hp + ch:hp + ch + self.H]
+
+    def _is(self, t, dtype, shape):
+        return t.dtype is dtype and tuple(t.shape) == tuple(shape) and t.is_contiguous() and t.device == self.dev
+
+    def _scan_state(self, state: dict, batch: int):
+        """state["ssd"], which the scan and its step take by address: refused unless it is as large as they read it."""
+        t, shape = state["ssd"], (batch, self.H, self.P, self.N)
+        kind = torch.float32 if self.path == "bf16" else torch.int8
+        if not self._is(t, kind, shape):
+            raise ssd.SsdError("SsdLayer", 1, f'state["ssd"] of a {self.path} layer has to be a contiguous {kind} tensor '
+                               f"{list(shape)} on {self.dev}; it is {t.dtype} {list(t.shape)} on {t.device}")
+        return t
 
     def zero_state(self, batch: int) -> dict:
         """The state of `batch` rows ahead of their first token."""
@@ -352,6 +372,7 @@ class SsdLayer:
 
     def _prefill(self, hidden, residual, state, lengths):
         b, L, d = hidden.shape
+        init = None if state is None else self._scan_state(state, b)
         T, w, new = b * L, self.w, self.new
         q, s = new(T, d, dtype=torch.int8), new(T, dtype=torch.float32)
         res = None if residual is None else residual.reshape(T, d)
@@ -365,7 +386,6 @@ class SsdLayer:
         ssd.ssd_conv_fwd_bf16(xbc, dt_raw, w["conv_w"], w.get("conv_b"), w["dt_bias"], lengths,
                               None if state is None else state["conv"], x, dt, B, C, conv)
         y = new(b, L, self.H, self.P)
-        init = None if state is None else state["ssd"]
         shape = ssd.SsdShape.of(b, L, self.H, self.P, self.G, self.N, self.chunk)
         ws = new(max(ssd.ssd_workspace_bytes(shape, self.path == "w8a8"), 256), dtype=torch.uint8)
         if self.path == "bf16":
@@ -403,7 +423,7 @@ class SsdLayerDecoder:
         self.qg, self.out = l.new(b, l.hp, dtype=i8), l.new(b, l.d)
         self.res = {t: l.new(b, l.d, dtype=t) for t in (torch.float32, torch.bfloat16)}
         self.z, self.xbc, self.dt_raw = l.slices(self.rows)
-        self.ssd = Decoder(state["ssd"], l.w["A"], l.w["D"], l.path, l.scales,
+        self.ssd = Decoder(l._scan_state(state, b), l.w["A"], l.w["D"], l.path, l.scales,
                            l.params.decay_shift if l.params is not None else 7)
 
     def step(self, hidden, residual=None, stream=None):

@@ -116,3 +116,38 @@ def test_an_expired_wait_of_the_scan_outlives_its_workspace(world, monkeypatch, 
         layer.check()
     assert err.value.status == 5
     layer.check()
+
+
+def _wrong_states(path, b):
+    good, other = (torch.float32, torch.int8) if path == "bf16" else (torch.int8, torch.float32)
+    z = lambda *s, t=good: torch.zeros(s, dtype=t)  # noqa: E731
+    return [z(b, H, P, N, t=other), z(b, H, P, N, t=torch.bfloat16), z(b - 1, H, P, N), z(b, H, P, N - 1),
+            z(b, H, P * N), z(b, H, N, P).transpose(2, 3), torch.zeros(b, H, P, N, dtype=good, device="meta")]
+
+
+@pytest.mark.parametrize("path", ["bf16", "w8a8"])
+def test_states_that_the_scan_would_read_past_are_refused(world, path):
+    """Another path's state, another batch's, one of other strides or elsewhere: nothing is launched."""
+    layer = make_layer(path)
+    hidden = torch.zeros(3, 2, D, dtype=torch.bfloat16)
+    for wrong in _wrong_states(path, 3):
+        state = {**layer.zero_state(3), "ssd": wrong}
+        with pytest.raises(ssd.SsdError) as err:
+            layer.prefill(hidden, None, state)
+        assert err.value.status == 1 and 'state["ssd"]' in str(err.value)
+        with pytest.raises(ssd.SsdError):
+            layer.decoder(state)
+    assert not world.calls
+    layer.prefill(hidden, None, layer.zero_state(3))
+    layer.decoder(layer.zero_state(3))
+
+
+@pytest.mark.parametrize("name,wrong", [("A", torch.ones(H, dtype=torch.float64)), ("A", torch.ones(H - 1)),
+                                        ("D", torch.ones(2 * H)[::2]), ("s_B", torch.ones(G + 1)),
+                                        ("s_C", torch.ones(G, dtype=torch.bfloat16)), ("s_x", torch.ones(H)),
+                                        ("s_s", torch.ones(H, P))])
+def test_scan_parameters_of_other_sizes_are_refused(name, wrong):
+    w, scales = make_weights(), make_scales()
+    (w if name in w else scales)[name] = wrong
+    with pytest.raises(ValueError, match=name):
+        runner.SsdLayer(w, (H, P, G, N), "w8a8", 64, scales)
