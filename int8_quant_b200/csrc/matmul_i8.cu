@@ -20,8 +20,10 @@
 //                       issue, 6.9 with two that load as well).
 //
 // Every wait is bounded; an expired wait raises the CTA's abort flag and records
-// SSD_ERR_TIMEOUT in the status word.
+// SSD_ERR_TIMEOUT in the status word.  Whichever role gave up, the CTA then waits, again with a
+// limit, for every copy and MMA that was issued: they use its shared memory and TMEM.
 #include "kernels.h"
+#include "ring.h"
 #include "tc.cuh"
 
 namespace ssd {
@@ -45,6 +47,16 @@ struct MatmulArgs {
     const int8_t* Wq;           // for it to prefetch
 };
 
+// After an abort: waits until the last copy into each stage has landed, `loaded(stage)` slices
+// having been asked for in the stage's turn, or until `deadline`.
+template <typename F>
+__device__ __forceinline__ void drain_ring(uint64_t* full, int stages, long long deadline, F loaded) {
+    for (int s = 0; s < stages; ++s) {
+        const long long u = ring_last_use(loaded(s), s, stages);
+        if (u >= 0) tc::mbar_wait(full + s, (uint32_t)(u & 1), deadline - clock64());
+    }
+}
+
 // ---------------------------------------------------------------- many tokens: CTA pairs
 
 namespace pair {
@@ -65,7 +77,8 @@ struct Layout {
     static constexpr int OFF_BAR = OFF_COL + kAcc * 2 * kTile * 4;
     static constexpr int B_FULL = 0, B_EMPTY = STAGES, B_AFULL = 2 * STAGES, B_AEMPTY = B_AFULL + kAcc,
                          B_DRAIN = B_AEMPTY + kAcc, NBAR = B_DRAIN + 1;
-    static constexpr int OFF_FLAG = OFF_BAR + NBAR * 8, OFF_TMEM = OFF_FLAG + 8, SMEM = OFF_TMEM + 8;
+    static constexpr int OFF_FLAG = OFF_BAR + NBAR * 8, OFF_TMEM = OFF_FLAG + 8, OFF_LOADED = OFF_TMEM + 8,
+                         SMEM = OFF_LOADED + 8;
     static_assert(SMEM + 1024 <= 227 * 1024, "shared memory of a CTA");
 };
 constexpr int kGroup = 8;                             // token tiles that share the weights while they are in L2
@@ -168,6 +181,7 @@ matmul_pair_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
     uint64_t* bar = reinterpret_cast<uint64_t*>(sm + Ly::OFF_BAR);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + Ly::OFF_FLAG);
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + Ly::OFF_TMEM);
+    long long* loaded = reinterpret_cast<long long*>(sm + Ly::OFF_LOADED);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = tc::cluster_rank();
     const bool leader = rank == 0;
@@ -200,7 +214,7 @@ matmul_pair_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         if (lane == 0) {
             int s = 0;
             uint32_t phase = 1;                                   // a fresh stage counts as free
-            int issued = 0;                                       // stages with a copy issued (up to kStages)
+            long long issued = 0;                                 // slices asked for
             bool ok = true;
             for (long long t = me; ok && t < tiles; t += pairs) {
                 int n0, t0;
@@ -214,19 +228,14 @@ matmul_pair_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                     const uint32_t full = tc::map_rank(tc::smem_u32(bar + B_FULL + s), 0);
                     tc::tma_load_2d_pair(sm + Ly::OFF_A + s * kOpBytes, &tm_q, full, k * kBK, t0);
                     tc::tma_load_2d_pair(sm + Ly::OFF_B + s * kOpBytes, &tm_w, full, k * kBK, n0);
-                    if (issued < kStages) ++issued;
+                    ++issued;
                     if (++s == kStages) {
                         s = 0;
                         phase ^= 1;
                     }
                 }
             }
-            if (!ok && leader)                                    // the copies in flight land before the CTA ends
-                for (int i = 0; i < issued; ++i) {
-                    // the phase of stage s's latest copy is the one before the free phase waited for next
-                    const int st = (s + kStages - 1 - i) % kStages;
-                    tc::mbar_wait(bar + B_FULL + st, st < s ? phase ^ 1 : phase, kDrainLimit);
-                }
+            *loaded = issued;
         }
         __syncwarp();
     } else if (warp == 1) {
@@ -264,11 +273,6 @@ matmul_pair_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                         phase ^= 1;
                     }
                 }
-            }
-            if (!ok) {                                            // the MMAs in flight end before TMEM is freed
-                if (tc::elect_one()) tc::mma_commit_pair(bar + B_DRAIN);
-                __syncwarp();
-                tc::mbar_wait(bar + B_DRAIN, 0, kDrainLimit);
             }
         }
     } else {
@@ -346,7 +350,26 @@ matmul_pair_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
     }
     tc::tc_fence_before();
     __syncthreads();
+    if (threadIdx.x == 0 && *abort_flag)                          // one CTA's abort is the pair's
+        tc::st_cluster_u32(tc::map_rank(tc::smem_u32(sm + Ly::OFF_FLAG), rank ^ 1), 1);
     tc::cluster_sync();                                           // no CTA leaves while the other may reach it
+    if (*abort_flag) {
+        // The roles of both CTAs are over.  The MMAs read both CTAs' shared memory and their commit
+        // arrives at both; both CTAs' copies count on the even CTA's barriers (a slice that only one
+        // of them asked for leaves its phase open: the deadline ends that wait, long after the copy).
+        if (warp == 1 && leader && tc::elect_one()) tc::mma_commit_pair(bar + B_DRAIN);
+        if (threadIdx.x == 0) {
+            const long long deadline = clock64() + kDrainLimit;
+            tc::mbar_wait(bar + B_DRAIN, 0, kDrainLimit);
+            if (leader) {
+                const long long other = tc::ld_cluster_s64(tc::map_rank(tc::smem_u32(loaded), 1));
+                const long long n = other > *loaded ? other : *loaded;
+                drain_ring(bar + B_FULL, kStages, deadline, [&](int) { return n; });
+            }
+        }
+        __syncthreads();
+        tc::cluster_sync();
+    }
     if (warp == 1) tc::tmem_dealloc_pair(tmem, kAcc * kTile);
 }
 
@@ -381,8 +404,8 @@ constexpr int kLoader2 = 3;                           // the second loading warp
 constexpr int kBudget = 98304;
 constexpr int alone_budget(int bn) { return bn < 64 ? 151552 : 212992; }
 constexpr int B_FULL = 0, B_EMPTY = kMaxStages, B_DONE = 2 * kMaxStages, NBAR = B_DONE + 1;
-constexpr int OFF_FLAG = NBAR * 8, OFF_TMEM = OFF_FLAG + 8, OFF_BUF = 1024;
-static_assert(OFF_TMEM + 8 <= OFF_BUF, "barriers in front of the stages");
+constexpr int OFF_FLAG = NBAR * 8, OFF_TMEM = OFF_FLAG + 8, OFF_LOADED = OFF_TMEM + 8, OFF_BUF = 1024;
+static_assert(OFF_LOADED + 8 <= OFF_BUF, "barriers in front of the stages");
 
 template <int BN>
 struct Layout {
@@ -421,6 +444,7 @@ matmul_few_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constan
     uint64_t* bar = reinterpret_cast<uint64_t*>(sm);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + OFF_FLAG);
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + OFF_TMEM);
+    int* loaded = reinterpret_cast<int*>(sm + OFF_LOADED);          // by each loading warp: its next slice
     uint8_t* buf = sm + OFF_BUF;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = SPLIT ? (int)tc::cluster_rank() : 0;
@@ -500,9 +524,7 @@ matmul_few_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constan
                 ready = j + Ly::ISSUE < k1 - k0 && tc::mbar_test(bar + B_EMPTY + s, phase);
                 load(j, at);
             }
-            if (!ok)                                              // the copies in flight land before the CTA ends
-                for (int i = j - stages; i < j; i += Ly::ISSUE)
-                    tc::mbar_wait(bar + B_FULL + i % stages, ((uint32_t)(i / stages)) & 1, kDrainLimit);
+            loaded[warp == 0 ? 0 : 1] = j;
         }
         __syncwarp();
     } else if (warp <= Ly::ISSUE) {
@@ -536,8 +558,7 @@ matmul_few_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constan
         ok = __all_sync(0xffffffffu, ok);
         if (lead) tc::mma_commit(bar + B_DONE);                     // every MMA issued, also when the loop gave up
         __syncwarp();
-        if (ok) ok = tc::wait_or_abort(bar + B_DONE, 0, abort_flag, p.status, kStatusTimeout);
-        else tc::mbar_wait(bar + B_DONE, 0, kDrainLimit);
+        if (ok) tc::wait_or_abort(bar + B_DONE, 0, abort_flag, p.status, kStatusTimeout);
         __syncwarp();
     }
     const bool in = warp >= 2 && ch < end;
@@ -615,6 +636,16 @@ matmul_few_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constan
         }
         // the others have read this CTA's sums; its stores need not be through (4 to 6% of a split call)
         tc::cluster_done();
+    }
+    // here, behind the code that every call fetches (ahead of the epilogue it took 0.25 us of a split call)
+    if (!ok) {
+        if (threadIdx.x == 0) {
+            const long long deadline = clock64() + kDrainLimit;
+            tc::mbar_wait(bar + B_DONE, 0, kDrainLimit);
+            drain_ring(bar + B_FULL, stages, deadline,
+                       [&](int s) { return (long long)min(loaded[s % Ly::ISSUE], k1 - k0); });
+        }
+        __syncthreads();
     }
     if (warp == 1) tc::tmem_dealloc(tmem, Ly::COLS);
 }

@@ -305,6 +305,14 @@ __device__ __forceinline__ int4 ld_cluster_s32x4(uint32_t addr) {
                  : "r"(addr));
     return v;
 }
+__device__ __forceinline__ long long ld_cluster_s64(uint32_t addr) {
+    long long v;
+    asm volatile("ld.shared::cluster.s64 %0, [%1];" : "=l"(v) : "r"(addr) : "memory");
+    return v;
+}
+__device__ __forceinline__ void st_cluster_u32(uint32_t addr, uint32_t v) {
+    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
 // Arrive on a barrier of another CTA of the cluster (an address from map_rank).
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
