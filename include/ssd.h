@@ -26,7 +26,7 @@
  *
  * Conventions (all entry points):
  *  - Tensors are dense, row-major, in the layouts given per argument; every device
- *    pointer must be 16-byte aligned.  bf16 tensors are passed as uint16_t bit
+ *    pointer must be 16-byte aligned unless its argument's text says less.  bf16 tensors are passed as uint16_t bit
  *    patterns.  The caller owns every buffer; the library allocates no memory.
  *  - Work is enqueued on `stream` and the call returns without synchronising.
  *    Argument and shape errors are detected on the host before anything is
@@ -361,6 +361,8 @@ ssd_status ssd_gated_rmsnorm_i8(int tokens, int d, const uint16_t* y, const uint
  * status : device int, left alone unless a device-side bounded wait expires, which writes
  *   SSD_ERR_TIMEOUT: clear it once, read it with ssd_workspace_status(status, stream).  Calls
  *   may share it.
+ * s_t, s_w and status may start at any element (4-byte alignment): a call on some tokens, some
+ *   channels, or with one of an array of status words.
  * k % 16 == 0, k <= 131056, 0 <= tokens <= 2^30 and 1 <= n <= 2^30, else
  * SSD_ERR_UNSUPPORTED (negative: SSD_ERR_INVALID_ARG). */
 ssd_status ssd_matmul_i8(int tokens, int k, int n, const int8_t* q, const float* s_t, const int8_t* Wq,

@@ -16,6 +16,7 @@ namespace {
 inline size_t align256(size_t v) { return (v + 255) & ~(size_t)255; }
 
 bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
+bool aligned4(const void* p) { return ((uintptr_t)p & 3u) == 0; }
 
 // Validates a shape; fills `d`.  Returns SSD_OK, SSD_ERR_INVALID_ARG or SSD_ERR_UNSUPPORTED.
 ssd_status make_dims(const ssd_shape* s, Dims* d) {
@@ -536,8 +537,8 @@ ssd_status ssd_matmul_i8(int tokens, int k, int n, const int8_t* q, const float*
     if (k % 16 != 0 || k > 131056 || tokens > (1 << 30) || n > (1 << 30)) return SSD_ERR_UNSUPPORTED;
     if (tokens == 0) return SSD_OK;
     if (!q || !s_t || !Wq || !s_w || !out || !status) return SSD_ERR_INVALID_ARG;
-    if (!aligned16(q) || !aligned16(s_t) || !aligned16(Wq) || !aligned16(s_w) || !aligned16(bias) || !aligned16(out) ||
-        !aligned16(status))
+    if (!aligned16(q) || !aligned4(s_t) || !aligned16(Wq) || !aligned4(s_w) || !aligned16(bias) || !aligned16(out) ||
+        !aligned4(status))
         return SSD_ERR_INVALID_ARG;
     SSD_STAGE("matmul_i8", launch_matmul_i8(tokens, k, n, q, s_t, Wq, s_w, bias, out, status, stream));
     return SSD_OK;

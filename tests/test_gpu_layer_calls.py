@@ -91,3 +91,20 @@ def test_status_is_kept_by_a_captured_prompt(torch_cuda):
         g.replay()
         layer.check()
         assert _same(got, ref)
+
+
+@pytest.mark.parametrize("T,N", [(40, 700), (1, 8), (1500, 2048), (1500, 2053)])
+def test_product_of_a_slice_of_tokens_and_channels(torch_cuda, T, N):
+    """Tokens from the second on, channels from the fourth on, one of several status words: what the whole call gives."""
+    torch = torch_cuda
+    import int8_quant_b200 as iq
+    g = torch.Generator(device="cuda").manual_seed(N)
+    q = torch.randint(-127, 128, (T + 1, 256), generator=g, device="cuda", dtype=torch.int8)
+    Wq = torch.randint(-127, 128, (N + 3, 256), generator=g, device="cuda", dtype=torch.int8)
+    s_t, s_w = torch.rand(T + 1, generator=g, device="cuda"), torch.rand(N + 3, generator=g, device="cuda")
+    words = torch.zeros(6, dtype=torch.int32, device="cuda")
+    whole, part = torch.empty(T + 1, N + 3, device="cuda").bfloat16(), torch.empty(T, N, device="cuda").bfloat16()
+    iq.ssd_matmul_i8(q, s_t, Wq, s_w, None, whole, words[:1])
+    iq.ssd_matmul_i8(q[1:], s_t[1:], Wq[3:], s_w[3:], None, part, words[5:])
+    assert torch.equal(part, whole[1:, 3:])
+    assert iq.ssd_workspace_status(words[5:]) == 0 and not words.any()

@@ -101,3 +101,13 @@ def test_binding_refuses_host_tensors():
         iq.ssd_conv_fwd_bf16(x, None, s, None, None, None, None, y, None, y, y, None)
     with pytest.raises(iq.SsdError):
         iq.ssd_conv_step_bf16(x, None, s, None, None, x, y[:, 0], None, y[:, 0], y[:, 0])
+
+
+def test_matmul_scales_and_status_need_their_elements_alignment():
+    f = iq.library().ssd_matmul_i8
+    good = [4, 64, 8, F, F, F, F, F, F, F, None]
+    for i in (4, 6, 9):
+        for p in (0x10002, 0x10001):
+            a = list(good)
+            a[i] = ctypes.c_void_p(p)
+            assert f(*a) == INVALID, (i, p)
