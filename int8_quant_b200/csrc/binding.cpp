@@ -299,4 +299,12 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, methods, n
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__binding(void) { return PyModule_Create(&module); }
+PyMODINIT_FUNC PyInit__binding(void) {
+    PyObject* m = PyModule_Create(&module);
+    // its calls read torch's objects directly, so it serves the torch that it was built for alone
+    if (m && PyModule_AddStringConstant(m, "torch_version", SSD_TORCH_VERSION) < 0) {
+        Py_DECREF(m);
+        return nullptr;
+    }
+    return m;
+}

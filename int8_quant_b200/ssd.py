@@ -292,11 +292,14 @@ def _binding():
     global _BINDING
     if _BINDING is None:
         _lib()
-        import torch  # noqa: F401  (its libraries are the binding's)
+        import torch                                  # its libraries are the binding's
         try:
             from . import _binding as m
         except ImportError as e:
             raise ImportError(f"_binding.so is not built or does not load; run int8_quant_b200/build.py ({e})") from e
+        if m.torch_version != torch.__version__:
+            raise ImportError(f"_binding.so was built for torch {m.torch_version}, not {torch.__version__}; run "
+                              "int8_quant_b200/build.py")
         _BINDING = m
     return _BINDING
 
