@@ -368,6 +368,17 @@ ssd_status ssd_gated_rmsnorm_i8(int tokens, int d, const uint16_t* y, const uint
 ssd_status ssd_matmul_i8(int tokens, int k, int n, const int8_t* q, const float* s_t, const int8_t* Wq,
                          const float* s_w, const float* bias, uint16_t* out, int* status, cudaStream_t stream);
 
+/* What ssd_matmul_i8 launches for these sizes on a GPU of `sms` SMs (>= 2; B200: 148), for tests and
+ * profiles: nothing is launched, and no GPU is needed.  No tokens: zeros. */
+typedef struct {
+    int pair;                           /* 1: a CTA pair per tile, persistent; 0: a cluster of `split` CTAs per tile */
+    int tile_tokens, tile_channels;
+    int split;                          /* CTAs that share a tile's k */
+    int stages, smem_bytes, tmem_columns;   /* of a CTA */
+    long long ctas;
+} ssd_matmul_plan;
+ssd_status ssd_matmul_i8_plan(int tokens, int k, int n, int sms, ssd_matmul_plan* plan);
+
 /* The short causal convolution ahead of the scan, with SiLU, and the scan's dt: over the
  * H*P + 2*G*N channels (x | B | C) of each batch row, with s the row's inputs and its
  * state's width - 1 inputs in front,

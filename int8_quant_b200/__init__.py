@@ -10,5 +10,5 @@ from .ssd import (SsdShape, SsdI8Params, SsdError, library, shape_of, i8_params,
                   ssd_workspace_status, ssd_profile_enable, ssd_profile_read, ssd_profile_reset, ssd_profile_filter,
                   ssd_selftest_bounded_wait, ssd_scan_fwd_bf16_from_state, ssd_scan_fwd_i8_from_state,
                   ssd_decode_step_bf16, ssd_decode_step_i8, ssd_out_proj_workspace_bytes, ssd_out_proj_i8,
-                  ssd_out_proj_status, ssd_add_rmsnorm_i8, ssd_gated_rmsnorm_i8, ssd_matmul_i8, ssd_conv_fwd_bf16,
-                  ssd_conv_step_bf16)
+                  ssd_out_proj_status, ssd_add_rmsnorm_i8, ssd_gated_rmsnorm_i8, ssd_matmul_i8, ssd_matmul_i8_plan,
+                  ssd_conv_fwd_bf16, ssd_conv_step_bf16)

@@ -529,18 +529,34 @@ ssd_status ssd_gated_rmsnorm_i8(int tokens, int d, const uint16_t* y, const uint
     return SSD_OK;
 }
 
-ssd_status ssd_matmul_i8(int tokens, int k, int n, const int8_t* q, const float* s_t, const int8_t* Wq,
-                         const float* s_w, const float* bias, uint16_t* out, int* status, cudaStream_t stream) {
+static ssd_status matmul_dims(int tokens, int k, int n) {
     if (tokens < 0 || k < 1 || n < 1) return SSD_ERR_INVALID_ARG;
     // rows of codes are TMA rows (16-byte strides); |sum| <= k * 128^2 stays in INT32; row
     // numbers past a tile's end stay in an int
-    if (k % 16 != 0 || k > 131056 || tokens > (1 << 30) || n > (1 << 30)) return SSD_ERR_UNSUPPORTED;
+    return k % 16 != 0 || k > 131056 || tokens > (1 << 30) || n > (1 << 30) ? SSD_ERR_UNSUPPORTED : SSD_OK;
+}
+
+ssd_status ssd_matmul_i8(int tokens, int k, int n, const int8_t* q, const float* s_t, const int8_t* Wq,
+                         const float* s_w, const float* bias, uint16_t* out, int* status, cudaStream_t stream) {
+    const ssd_status st = matmul_dims(tokens, k, n);
+    if (st != SSD_OK) return st;
     if (tokens == 0) return SSD_OK;
     if (!q || !s_t || !Wq || !s_w || !out || !status) return SSD_ERR_INVALID_ARG;
     if (!aligned16(q) || !aligned4(s_t) || !aligned16(Wq) || !aligned4(s_w) || !aligned16(bias) || !aligned16(out) ||
         !aligned4(status))
         return SSD_ERR_INVALID_ARG;
     SSD_STAGE("matmul_i8", launch_matmul_i8(tokens, k, n, q, s_t, Wq, s_w, bias, out, status, stream));
+    return SSD_OK;
+}
+
+ssd_status ssd_matmul_i8_plan(int tokens, int k, int n, int sms, ssd_matmul_plan* plan) {
+    if (!plan || sms < 2) return SSD_ERR_INVALID_ARG;
+    const ssd_status st = matmul_dims(tokens, k, n);
+    if (st != SSD_OK) return st;
+    memset(plan, 0, sizeof *plan);
+    if (tokens == 0) return SSD_OK;
+    const MatmulPlan p = plan_matmul_i8(tokens, k, n, sms);
+    *plan = ssd_matmul_plan{p.pair, p.tile_tokens, p.tile_channels, p.split, p.stages, p.smem, p.tmem_columns, p.ctas};
     return SSD_OK;
 }
 

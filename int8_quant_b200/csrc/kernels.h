@@ -97,6 +97,16 @@ cudaError_t launch_gated_rmsnorm_i8(int T, int d, const uint16_t* y, const uint1
 // out [T,N] (bf16) = (q [T,K] Wq [N,K]^T) * s_t[t] * s_w[n] + bias[n] (matmul_i8.cu).
 cudaError_t launch_matmul_i8(int T, int K, int N, const int8_t* q, const float* s_t, const int8_t* Wq,
                              const float* s_w, const float* bias, uint16_t* out, int* status, cudaStream_t st);
+// What launch_matmul_i8 launches on a GPU of `sms` SMs.
+struct MatmulPlan {
+    bool pair;                  // on CTA pairs, else matmul_few_kernel
+    int tile_tokens, tile_channels;
+    int split;                  // CTAs that share a tile's K
+    int stages, smem;           // of a CTA's ring; shared memory, bytes
+    int tmem_columns;
+    long long ctas;
+};
+MatmulPlan plan_matmul_i8(int T, int K, int N, int sms);
 
 // The short causal convolution ahead of the scan (conv.cu).
 struct ConvDims {

@@ -669,13 +669,17 @@ int tile_rows(int N, int tiles_t, int S, int sms) {
     return rows;
 }
 
+// Stages of a CTA's ring, `nk` slices of K split S ways.
+template <int BN>
+int ring_stages(long long ctas, int rows, int nk, int S, int sms) {
+    return Layout<BN>::stages(rows, (nk - 1) / S + 1, ctas <= resident(S, 1, sms) ? alone_budget(BN) : kBudget);
+}
+
 template <int BN>
 cudaError_t launch(const CUtensorMap& mw, const CUtensorMap& mq, const MatmulArgs& p, int S, cudaStream_t st) {
     using Ly = Layout<BN>;
     const long long ctas = (long long)p.tiles_n * p.tiles_t * S;
-    const int nk = (p.K - 1) / kBK + 1;
-    const int stages = Ly::stages(p.rows, (nk - 1) / S + 1,
-                                  ctas <= resident(S, 1, device_sm_count()) ? alone_budget(BN) : kBudget);
+    const int stages = ring_stages<BN>(ctas, p.rows, (p.K - 1) / kBK + 1, S, device_sm_count());
     const auto kernel = S > 1 ? matmul_few_kernel<BN, true> : matmul_few_kernel<BN, false>;
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                1024 + OFF_BUF + alone_budget(BN));
@@ -716,7 +720,10 @@ double pair_estimate(long long tiles, int nk, bool sectors, bool aligned, int sm
     return 3.3 + turns * (nk * (sectors ? 0.30 : 0.36) + (aligned ? 1.9 : 3.9));
 }
 
-}  // namespace
+struct Choice {
+    bool pair;                  // matmul_pair_kernel
+    int bn, rows, S;            // else matmul_few_kernel: its tile's tokens and channels, its split of K
+};
 
 // Which kernel, and how many ranks: matmul_few_kernel up to 64 tokens, else the one that is
 // expected to take less; the split S that is (all CTAs resident at a time).  Over 308 sizes, most
@@ -725,16 +732,13 @@ double pair_estimate(long long tiles, int nk, bool sectors, bool aligned, int sm
 // microseconds with S = 1, 2, 4, 8 and on pairs:
 //    8 x 5120 -> 2560   6.8  6.5  5.1  5.3 15.7      64 x 4096 -> 2048   6.8  6.9  5.2  6.6  13.7
 //    8 x 8192 -> 4096   9.9  9.5  8.3  8.8 24.0     512 x 8192 -> 4096  19.2 19.5 28.7 46.5  23.5
-cudaError_t launch_matmul_i8(int T, int K, int N, const int8_t* q, const float* s_t, const int8_t* Wq,
-                             const float* s_w, const float* bias, uint16_t* out, int* status, cudaStream_t st) {
-    CUtensorMap mw, mq;
-    MatmulArgs p{T, K, N, 0, 0, s_t, s_w, bias, out, status, 0, Wq};
-    const int sms = device_sm_count(), nk = tiles_of(K, kBK);
+Choice choose(int T, int K, int N, int sms) {
+    const int nk = tiles_of(K, kBK);
     const int bn = T <= 16 ? 16 : T <= 32 ? 32 : T <= 64 ? 64 : 128;
     const int few_t = tiles_of(T, bn);
     const long long pair_tiles = (long long)tiles_of(T, pair::kTile) * tiles_of(N, pair::kTile);
     const bool sectors = K % 32 == 0;
-    int S = 1;
+    Choice best{false, bn, 0, 1};
     double few_us = 0.0;
     for (int c : {1, 2, 4, 8}) {
         if (c > 1 && (c > nk || (long long)tiles_of(N, few::kRows) * few_t * c * 4 > 7LL * sms)) break;
@@ -742,19 +746,54 @@ cudaError_t launch_matmul_i8(int T, int K, int N, const int8_t* q, const float* 
         const double us = few_estimate((long long)tiles_of(N, rows) * few_t, rows, nk, bn, c, sectors, sms);
         if (c == 1 || us < few_us) {
             few_us = us;
-            S = c;
-            p.rows = rows;
+            best.S = c;
+            best.rows = rows;
         }
     }
-    const double pair_us = pair_estimate(pair_tiles, nk, sectors, N % 8 == 0, sms);
-    if (T <= 64 || few_us <= pair_us) {
-        p.tiles_n = tiles_of(N, p.rows);
-        p.tiles_t = few_t;
-        if (!operand_map(&mw, Wq, N, K, p.rows) || !operand_map(&mq, q, T, K, bn)) return cudaErrorInvalidValue;
-        if (bn == 16) return few::launch<16>(mw, mq, p, S, st);
-        if (bn == 32) return few::launch<32>(mw, mq, p, S, st);
-        if (bn == 64) return few::launch<64>(mw, mq, p, S, st);
-        return few::launch<128>(mw, mq, p, S, st);
+    best.pair = T > 64 && few_us > pair_estimate(pair_tiles, nk, sectors, N % 8 == 0, sms);
+    return best;
+}
+
+template <int BN>
+MatmulPlan few_plan(const Choice& c, int T, int K, int N, int sms) {
+    const long long ctas = (long long)tiles_of(N, c.rows) * tiles_of(T, BN) * c.S;
+    const int stages = few::ring_stages<BN>(ctas, c.rows, tiles_of(K, kBK), c.S, sms);
+    return MatmulPlan{false, BN, c.rows, c.S, stages, few::Layout<BN>::smem(c.rows, stages), few::Layout<BN>::COLS, ctas};
+}
+
+template <bool ALIGNED>
+MatmulPlan pair_plan(int T, int N, int sms) {
+    const long long tiles = (long long)tiles_of(T, pair::kTile) * tiles_of(N, pair::kTile), most = sms / 2;
+    using Ly = pair::Layout<ALIGNED>;
+    return MatmulPlan{true, pair::kTile, pair::kTile, 1, Ly::STAGES, Ly::SMEM + 1024, pair::kAcc * pair::kTile,
+                      2 * (tiles < most ? tiles : most)};
+}
+
+}  // namespace
+
+MatmulPlan plan_matmul_i8(int T, int K, int N, int sms) {
+    const Choice c = choose(T, K, N, sms);
+    if (c.pair) return N % 8 == 0 ? pair_plan<true>(T, N, sms) : pair_plan<false>(T, N, sms);
+    if (c.bn == 16) return few_plan<16>(c, T, K, N, sms);
+    if (c.bn == 32) return few_plan<32>(c, T, K, N, sms);
+    if (c.bn == 64) return few_plan<64>(c, T, K, N, sms);
+    return few_plan<128>(c, T, K, N, sms);
+}
+
+cudaError_t launch_matmul_i8(int T, int K, int N, const int8_t* q, const float* s_t, const int8_t* Wq,
+                             const float* s_w, const float* bias, uint16_t* out, int* status, cudaStream_t st) {
+    CUtensorMap mw, mq;
+    MatmulArgs p{T, K, N, 0, 0, s_t, s_w, bias, out, status, 0, Wq};
+    const Choice c = choose(T, K, N, device_sm_count());
+    if (!c.pair) {
+        p.rows = c.rows;
+        p.tiles_n = tiles_of(N, c.rows);
+        p.tiles_t = tiles_of(T, c.bn);
+        if (!operand_map(&mw, Wq, N, K, c.rows) || !operand_map(&mq, q, T, K, c.bn)) return cudaErrorInvalidValue;
+        if (c.bn == 16) return few::launch<16>(mw, mq, p, c.S, st);
+        if (c.bn == 32) return few::launch<32>(mw, mq, p, c.S, st);
+        if (c.bn == 64) return few::launch<64>(mw, mq, p, c.S, st);
+        return few::launch<128>(mw, mq, p, c.S, st);
     }
     if (!operand_map(&mw, Wq, N, K, pair::kRows) || !operand_map(&mq, q, T, K, pair::kRows)) return cudaErrorInvalidValue;
     p.tiles_n = tiles_of(N, pair::kTile);

@@ -26,7 +26,7 @@ EXPORTS = ("ssd_status_string", "ssd_last_cuda_error", "ssd_workspace_bytes", "s
            "ssd_scan_fwd_bf16_from_state", "ssd_scan_fwd_i8_from_state", "ssd_decode_step_bf16", "ssd_profile_filter",
            "ssd_decode_step_i8", "ssd_out_proj_workspace_bytes", "ssd_out_proj_i8", "ssd_out_proj_status",
            "ssd_static_scratch_status", "ssd_add_rmsnorm_i8", "ssd_gated_rmsnorm_i8", "ssd_matmul_i8",
-           "ssd_conv_fwd_bf16", "ssd_conv_step_bf16")
+           "ssd_matmul_i8_plan", "ssd_conv_fwd_bf16", "ssd_conv_step_bf16")
 
 # Size of the library's fixed device scratch used by ssd_scan_fwd_bf16_static.
 STATIC_SCRATCH_BYTES = 32 << 20
@@ -48,6 +48,11 @@ class SsdShape(ctypes.Structure):
 class SsdI8Params(ctypes.Structure):
     _fields_ = [("s_B", ctypes.c_void_p), ("s_C", ctypes.c_void_p), ("s_x", ctypes.c_void_p),
                 ("s_s", ctypes.c_void_p), ("decay_shift", ctypes.c_int), ("storage", ctypes.c_int)]
+
+
+class SsdMatmulPlan(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int) for n in ("pair", "tile_tokens", "tile_channels", "split", "stages", "smem_bytes",
+                                            "tmem_columns")] + [("ctas", ctypes.c_longlong)]
 
 
 SSD_STORAGE_ACS_FP16 = 1
@@ -130,6 +135,8 @@ def _lib():
         lib.ssd_gated_rmsnorm_i8.argtypes = [I, I, P, P, L, P, F, P, P, P, P]
         lib.ssd_matmul_i8.restype = I
         lib.ssd_matmul_i8.argtypes = [I, I, I, P, P, P, P, P, P, P, P]
+        lib.ssd_matmul_i8_plan.restype = I
+        lib.ssd_matmul_i8_plan.argtypes = [I, I, I, I, ctypes.POINTER(SsdMatmulPlan)]
         lib.ssd_conv_fwd_bf16.restype = I
         lib.ssd_conv_fwd_bf16.argtypes = [sp, I, P, P, L, P, P, P, P, P, P, P, P, P, P, P]
         lib.ssd_conv_step_bf16.restype = I
@@ -332,6 +339,13 @@ def ssd_matmul_i8(q, s_t, Wq, s_w, bias, out, status, stream=None):
     bad = (_BINDING or _binding()).matmul_i8(q, s_t, Wq, s_w, bias, out, status, _handle(stream))
     if bad:
         raise SsdError("ssd_matmul_i8", *bad)
+
+
+def ssd_matmul_i8_plan(tokens: int, k: int, n: int, sms: int = 148) -> SsdMatmulPlan:
+    """What ssd_matmul_i8 launches for these sizes on a GPU of `sms` SMs."""
+    plan = SsdMatmulPlan()
+    _check("ssd_matmul_i8_plan", _lib().ssd_matmul_i8_plan(int(tokens), int(k), int(n), int(sms), ctypes.byref(plan)))
+    return plan
 
 
 def ssd_conv_fwd_bf16(xbc, dt_raw, weight, bias, dt_bias, lengths, initial_state, x, dt, B, C, final_state,
