@@ -353,6 +353,8 @@ class SsdLayer:
         Returns (the layer's output [b, L, d] bf16, the residual to hand on, the state after each row's last
         token).  Outputs behind a row's last token mean nothing.  Runs on the layer's device, and there on `stream` (a
         torch stream or a handle; None: the current one), to which the buffers and outputs belong as well."""
+        if stream is None and torch.cuda.current_device() == self.index:
+            return self._prefill(hidden, residual, state, lengths)
         with self._on(stream):
             return self._prefill(hidden, residual, state, lengths)
 
@@ -387,7 +389,7 @@ class SsdLayer:
                               None if state is None else state["conv"], x, dt, B, C, conv)
         y = new(b, L, self.H, self.P)
         shape = ssd.SsdShape.of(b, L, self.H, self.P, self.G, self.N, self.chunk)
-        ws = new(max(ssd.ssd_workspace_bytes(shape, self.path == "w8a8"), 256), dtype=torch.uint8)
+        ws = new((max(ssd.ssd_workspace_bytes(shape, self.path == "w8a8"), 256) + 3) // 4, dtype=torch.int32)
         if self.path == "bf16":
             fin = new(b, self.H, self.P, self.N, dtype=torch.float32)
             ssd.ssd_scan_fwd_bf16_from_state(shape, x, dt, w["A"], B, C, w["D"], init, y, fin, ws)
@@ -399,7 +401,7 @@ class SsdLayer:
         qg, out = new(T, self.hp, dtype=torch.int8), new(b, L, d)
         if b > 0:
             # the scan's error word ends with its workspace; an atomic maximum, as other streams' calls may do the same
-            self.status.scatter_reduce_(0, self._word0, ws[:4].view(torch.int32), "amax")
+            self.status.scatter_reduce_(0, self._word0, ws[:1], "amax")
         ssd.ssd_gated_rmsnorm_i8(y.view(T, self.hp), rows.view(T, self.E)[:, :self.hp], w["gate_norm"], self.eps, qg, s)
         ssd.ssd_matmul_i8(qg, s, w["out_q"], w["out_s"], w.get("out_corr"), out.view(T, d), self.status)
         return out, res_out.view(b, L, d), {"conv": conv, "ssd": fin}
