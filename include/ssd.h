@@ -322,7 +322,9 @@ ssd_status ssd_out_proj_status(void* workspace, int tokens, int d_inner, cudaStr
  * that forms them (the convolution's two entry points agree bit for bit).  Outputs must not
  * overlap inputs or each other unless an argument's text allows it.  The kernels may start
  * while the one ahead of them in the stream ends (programmatic stream serialisation); they
- * read and write nothing before it has. */
+ * read no value and write nothing before it has.  ssd_matmul_i8 may by then have asked for Wq
+ * to be brought to L2: Wq may still be written by the kernel ahead, and has to be mapped memory
+ * from the call on, as stream-ordered allocation in front of the call makes it. */
 
 /* Residual addition and RMSNorm of each token, to INT8 codes with one scale per token:
  *   v = x + residual              (fp32; residual null: v = x), kept as residual_out

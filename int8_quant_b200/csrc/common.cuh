@@ -21,10 +21,11 @@ enum : int { kStatusOk = 0, kStatusTimeout = 5 };
 
 // ---------------------------------------------------------------- programmatic launches
 // A kernel launched with launch_programmatic may start while the one ahead of it in the stream
-// still runs: it reads and writes nothing of global memory in front of grid_wait(), which
-// returns once that kernel (and so all ahead of it) is done.  What it reads may have been
-// written during its own life, so it uses no read-only loads (__ldg).  grid_release() lets the
-// next such kernel start.
+// still runs: it reads no value and writes nothing of global memory in front of grid_wait(), which
+// returns once that kernel (and so all ahead of it) is done.  (A prefetch to L2 reads no value: L2
+// is where the kernel ahead writes, so a later read sees what it wrote.  It needs mapped memory.)
+// What it reads may have been written during its own life, so it uses no read-only loads (__ldg).
+// grid_release() lets the next such kernel start.
 __device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void grid_release() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 

@@ -634,7 +634,8 @@ matmul_few_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constan
                 }
             }
         }
-        // the others have read this CTA's sums; its stores need not be through (4 to 6% of a split call)
+        // The others have read this CTA's sums: each sum that a warp loaded goes into f[0] of its lane 0,
+        // whose channel n0 exists, and is stored.  Its stores need not be through (4 to 6% of a split call).
         tc::cluster_done();
     }
     // here, behind the code that every call fetches (ahead of the epilogue it took 0.25 us of a split call)

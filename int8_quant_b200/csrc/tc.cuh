@@ -291,8 +291,11 @@ __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release;" ::: "memory");
     asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
 }
-// Waits until every thread of the cluster is here, without waiting for its stores: reads whose
-// values were used are over.
+// Waits until every thread of the cluster is here, without waiting for its stores.  The relaxed
+// arrival orders nothing, so a CTA may leave (and its shared memory go to another) only because
+// every remote read in front of this is over: its value has been used, by some lane of the warp that
+// read it, in an instruction ahead of the arrival.  An editor who reads further ahead than is used,
+// or drops the use, needs cluster_sync.
 __device__ __forceinline__ void cluster_done() {
     asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory");
     asm volatile("barrier.cluster.wait;" ::: "memory");
