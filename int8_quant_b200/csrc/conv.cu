@@ -15,8 +15,8 @@
 // slid along registers, without the staging, 344.  Blocks behind those of the convolution form
 // dt and the final state.
 // conv_step_kernel: one token; a thread owns 8 channels of one or two batch rows and shifts
-// their state in place (8 x 5376 channels in a graph 1.7 us, the launch; 128 x 10240, 21 MB,
-// 3.7 us = 5.7 TB/s from L2).
+// their state in place (8 x 5376 channels in a graph 1.8 us, the launch; 128 x 10240, 21 MB,
+// 3.8 us = 5.5 TB/s from L2).
 #include "kernels.h"
 
 namespace ssd {
@@ -288,7 +288,7 @@ static cudaError_t launch_step(const ConvDims& d, ConvArgs a, uint16_t* state, c
 }
 
 // Two rows a thread where one each would be more threads than the GPU holds at a time (128 x
-// 5376 channels 3.3 us with one, 3.4 with two; 128 x 10240 4.2, 3.7; 256 x 10240 7.1, 6.1).
+// 5376 channels 3.4 us with one, 3.6 with two; 128 x 10240 4.3, 3.8; 256 x 10240 7.0, 5.9).
 cudaError_t launch_conv_step(const ConvDims& d, const ConvIn& in, uint16_t* state, const ConvOut& out,
                              cudaStream_t st) {
     const ConvArgs a = conv_args(d, in, out);

@@ -16,8 +16,9 @@
 //                       by the weights' way in: a barrier's answer takes some 60 cycles and a
 //                       slice's MMAs 130, so that one warp that loads and one that issues spent
 //                       450 cycles a slice, whatever its bytes.  Two of each spend under 200
-//                       (unsplit 8 x 5120 -> 2560, from L2: 11.5 us with one, 9.2 with two that
-//                       issue, 6.9 with two that load as well).
+//                       (unsplit 8 x 5120 -> 2560, from L2, when they were added: 11.5 us with
+//                       one, 9.2 with two that issue, 6.9 with two that load as well; 6.8 now).
+// Times in this file: one call among many in a graph, the weights in HBM unless said.
 //
 // Every wait is bounded; an expired wait raises the CTA's abort flag and records
 // SSD_ERR_TIMEOUT in the status word.  Whichever role gave up, the CTA then waits, again with a
@@ -121,7 +122,7 @@ __device__ __forceinline__ void fill_box(const uint32_t (&v)[32], float st, cons
 // shared memory shifted by the elements that its first lacks to a 16-byte boundary, so that
 // the row's aligned vectors are vectors there; then 8 lanes store a row's, and its up to 7
 // elements in front of and behind them one by one.  4096 x 1024 -> 8193 takes 51 us (8208,
-// aligned, 34); 32 two-byte stores a row, from a tile with the channels in its rows, took 66.
+// aligned, 33; weights from L2); 32 two-byte stores a row, from a tile with the channels in its rows, took 66.
 __device__ __forceinline__ void store_shifted(const uint32_t (&lo)[32], const uint32_t (&hi)[32], float st,
                                               const float* sw, const float* bias, uint8_t* buf, int lane,
                                               uint16_t* dst, int rows, int cols) {
@@ -393,14 +394,14 @@ namespace few {
 
 constexpr int kRows = 128;                            // rows of the MMA; a tile has up to as many channels
 constexpr int kMaxStages = 16, kLeastRows = 64;
-// Lines that a CTA prefetches at most (8 x 4096 -> 18560 14.6 us with all 4096, 13.6 so; 64 tokens
-// 17.2, 15.3; 64 x 5120 -> 2560 7.0 with 768, 6.6 with all its 1280).
+// Lines that a CTA prefetches at most (8 x 4096 -> 18560 14.5 us with all 4096, 13.0 so; 64 tokens
+// 15.8, 14.3; 64 x 5120 -> 2560 6.7 with 768, 6.2 with all its 1280).
 constexpr int kAhead = 1280;
 constexpr int kLoader2 = 3;                           // the second loading warp, until its epilogue
 // Shared memory for stages where two CTAs share an SM, and where none has to: the bytes on their
-// way bound an SM's rate (8 x 5120 -> 2560 7.5 us with 96 KB, 5.7 with 148, 5.6 with 208; 256 x 8192
-// -> 4096 16.0 with 148, 14.7 with 208).  For few tokens 148 KB leave room for the next kernels'
-// CTAs (a decode step of batch 1 21.55 us, 21.63 with 208).
+// way bound an SM's rate (8 x 5120 -> 2560 6.8 us with 96 KB, 5.2 with 148 or 208; 256 x 8192 -> 4096
+// 18.6, 15.6 and 14.4).  For few tokens 148 KB leave room for the next kernels' CTAs (a 2560-feature
+// layer's decode step, bf16 scan: batch 1 20.7 us, 20.8 with 208; batch 8 26.9, 27.1).
 constexpr int kBudget = 98304;
 constexpr int alone_budget(int bn) { return bn < 64 ? 151552 : 212992; }
 constexpr int B_FULL = 0, B_EMPTY = kMaxStages, B_DONE = 2 * kMaxStages, NBAR = B_DONE + 1;
@@ -491,8 +492,9 @@ matmul_few_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constan
     const uint32_t tmem = *tmem_slot;
 
     // The epilogue's factors, asked for ahead of everything that it waits for (8 x 5120 -> 2560
-    // 5.7 us without, 5.4 so; with the split at run time 64 x 2560 -> 10576 7.9 us, 7.1 so).  Unsplit, a thread has a channel, and lane i the scale of the token
-    // 16 part + i % 16; split, a lane has four channels, and lane i the scale of its warp's i-th token
+    // 5.7 us without, 5.4 so, and 64 x 2560 -> 10576 7.9 us with the split at run time, 7.1 so, when
+    // these were added; 5.2 and 7.2 now).  Unsplit, a thread has a channel, and lane i the scale of
+    // the token 16 part + i % 16; split, a lane has four channels, and lane i the scale of its warp's i-th token
     // (at most BN / kEpi).
     const int quarter = warp & 3, row = quarter * 32 + lane, ch = n0 + row, part = (warp - 2) / 4;
     const int c4 = SPLIT ? n0 + 4 * lane : ch, end = min(p.N, n0 + p.rows), live = min(BN, p.T - t0);
@@ -653,14 +655,15 @@ matmul_few_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constan
 
 // CTAs of a call that are resident together with `per` on each SM.  Clusters of more than two
 // leave some SMs of their part of the GPU unused (35 of four with an SM a CTA run in two turns:
-// 5 x 4464 -> 4480 13.0 us, 8.0 with two CTAs an SM).
+// 5 x 4464 -> 4480 10.9 us, 7.2 with two CTAs an SM).
 long long resident(int S, int per, int sms) { return (long long)per * sms * (S > 2 ? 7 : 8) / 8; }
 
 // Channels of a tile.  Unsplit, as few (from 64 on) as let all CTAs still be resident, on an SM
-// each if those of 128 are, else on two, so that every SM loads its share (8 x 2560 -> 10576 6.9 us
-// with 133 tiles, 7.7 with 83; 8 x 1024 -> 4376 3.7 with 128 channels, 4.0 with 64, 4.6 with 32).
+// each if those of 128 are, else on two, so that every SM loads its share (8 x 2560 -> 10576 6.5 us
+// with 133 tiles of 80, 7.3 with 83 of 128 or 166 of 64).  Small weights would rather have fewer
+// (8 x 1024 -> 4376 3.26 us with 128 channels, 3.44 with 64, 4.36 with 32).
 // Split, more CTAs cost more in clusters and joins than they load sooner (8 x 5120 -> 2560, S = 4:
-// 6.0 with 80 channels or 128; a layer's decode step 25.2, 24.8).
+// 5.6 with 80 channels, 5.2 with 128; a layer's decode step of batch 8 25.1, 24.6).
 int tile_rows(int N, int tiles_t, int S, int sms) {
     if (S > 1) return kRows;
     const auto ctas = [&](int rows) { return (long long)((N - 1) / rows + 1) * tiles_t; };
@@ -727,12 +730,13 @@ struct Choice {
 };
 
 // Which kernel, and how many ranks: matmul_few_kernel up to 64 tokens, else the one that is
-// expected to take less; the split S that is (all CTAs resident at a time).  Over 308 sizes, most
-// drawn at random (1 to 1024 tokens, K to 8192, N to 18560), the choice takes 1.2% longer than the
-// best of all in the geometric mean.  Measured in a graph, each call's weights in HBM,
-// microseconds with S = 1, 2, 4, 8 and on pairs:
-//    8 x 5120 -> 2560   6.8  6.5  5.1  5.3 15.7      64 x 4096 -> 2048   6.8  6.9  5.2  6.6  13.7
-//    8 x 8192 -> 4096   9.9  9.5  8.3  8.8 24.0     512 x 8192 -> 4096  19.2 19.5 28.7 46.5  23.5
+// expected to take less; the split S that is (all CTAs resident at a time).  Over 48 sizes of usual
+// widths the choice takes 1.2% longer than the best of all in the geometric mean, over 120 sizes that
+// the estimates were not fitted to (1 to 1024 tokens, K to 8192, N to 18560) 1.4%; 23% at most, at
+// 512 x 2048 -> 1024.  Measured in a graph, each call's weights in HBM, microseconds with S = 1, 2, 4,
+// 8 and on pairs:
+//    8 x 5120 -> 2560   6.9  6.7  5.2  5.4 15.8      64 x 4096 -> 2048   6.9  7.0  5.3  6.6  13.8
+//    8 x 8192 -> 4096  10.0  9.7  8.3  9.0 23.6     512 x 8192 -> 4096  19.7 20.3 29.4 47.8  24.7
 Choice choose(int T, int K, int N, int sms) {
     const int nk = tiles_of(K, kBK);
     const int bn = T <= 16 ? 16 : T <= 32 ? 32 : T <= 64 ? 64 : 128;

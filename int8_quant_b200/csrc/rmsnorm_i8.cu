@@ -14,7 +14,9 @@
 // of 8 features a thread, all loads issued before anything else; many small CTAs resident on
 // an SM cover each other's barrier.  Measured, in a graph (6.53 TB/s is the copy bandwidth):
 //   65536 x 2560, fp32 residual   265 us = 7.0 TB/s, with values 318 us = 6.9 TB/s
-//   16384 x 5120, gate             68 us = 6.2 TB/s, with values  89 us = 6.6 TB/s
+//   65536 x 2560, bf16 residual   176 us = 6.7 TB/s, with values 221 us = 6.8 TB/s
+//   65536 x 2560, no residual     111 us = 4.5 TB/s, with values 140 us = 6.0 TB/s
+//   16384 x 5120, gate             67 us = 6.3 TB/s, with values  89 us = 6.6 TB/s
 // The gate spends two special-function instructions a feature (exponential, reciprocal); with
 // packed fp32 arithmetic it takes half the instructions of the plain form (95 us).  A
 // persistent grid that loads the next token ahead needs twice the registers and was slower:
