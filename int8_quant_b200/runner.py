@@ -435,7 +435,8 @@ class SsdLayerDecoder:
         if torch.cuda.current_device() != l.index:       # the scan's step launches on the current device
             with torch.cuda.device(l.index):
                 return self.step(hidden, residual, stream)
-        res = self.res[torch.float32 if residual is None else residual.dtype]
+        # (a residual of another type is refused by the call)
+        res = self.res[torch.bfloat16 if residual is not None and residual.dtype is not torch.float32 else torch.float32]
         ssd.ssd_add_rmsnorm_i8(hidden, residual, w["norm"], l.eps, res, self.q, self.s, stream=stream)
         ssd.ssd_matmul_i8(self.q, self.s, w["in_q"], w["in_s"], None, self.rows, l.status, stream)
         ssd.ssd_conv_step_bf16(self.xbc, self.dt_raw, w["conv_w"], w.get("conv_b"), w["dt_bias"], self.state["conv"],

@@ -108,3 +108,14 @@ def test_product_of_a_slice_of_tokens_and_channels(torch_cuda, T, N):
     iq.ssd_matmul_i8(q[1:], s_t[1:], Wq[3:], s_w[3:], None, part, words[5:])
     assert torch.equal(part, whole[1:, 3:])
     assert iq.ssd_workspace_status(words[5:]) == 0 and not words.any()
+
+
+def test_residual_of_another_type_is_refused(torch_cuda):
+    torch = torch_cuda
+    import int8_quant_b200 as iq
+    layer = _layer(torch, "bf16")
+    hidden, res = _hidden(torch, 1, 2, 3, D), torch.zeros(2, 3, D, device="cuda", dtype=torch.float16)
+    with pytest.raises(iq.SsdError, match="residual"):
+        layer.prefill(hidden, res)
+    with pytest.raises(iq.SsdError, match="residual"):
+        layer.decoder(layer.zero_state(2)).step(hidden[:, 0].contiguous(), res[:, 0].contiguous())

@@ -151,3 +151,14 @@ def test_scan_parameters_of_other_sizes_are_refused(name, wrong):
     (w if name in w else scales)[name] = wrong
     with pytest.raises(ValueError, match=name):
         runner.SsdLayer(w, (H, P, G, N), "w8a8", 64, scales)
+
+
+def test_a_residual_of_another_type_reaches_the_calls_own_check(world, monkeypatch):
+    """... which refuses it with its reason, from the prompt and from the step."""
+    layer, seen = make_layer("bf16"), []
+    layer.index = 0
+    monkeypatch.setattr(ssd, "ssd_add_rmsnorm_i8", lambda x, res, *a, **k: seen.append(res.dtype))
+    res = torch.zeros(2, D, dtype=torch.float16)
+    layer.prefill(torch.zeros(2, 1, D, dtype=torch.bfloat16), res[:, None])
+    layer.decoder(layer.zero_state(2)).step(torch.zeros(2, D, dtype=torch.bfloat16), res)
+    assert seen == [torch.float16] * 2
