@@ -377,9 +377,10 @@ class SsdLayer:
         init = None if state is None else self._scan_state(state, b)
         T, w, new = b * L, self.w, self.new
         q, s = new(T, d, dtype=torch.int8), new(T, dtype=torch.float32)
-        res = None if residual is None else residual.reshape(T, d)
+        # a slice of a longer batch is copied (so is one of a single token, which reshape leaves as it is)
+        hidden, res = hidden.reshape(T, d).contiguous(), None if residual is None else residual.reshape(T, d).contiguous()
         res_out = new(T, d, dtype=torch.float32 if res is None else res.dtype)
-        ssd.ssd_add_rmsnorm_i8(hidden.reshape(T, d), res, w["norm"], self.eps, res_out, q, s)
+        ssd.ssd_add_rmsnorm_i8(hidden, res, w["norm"], self.eps, res_out, q, s)
         rows = new(b, L, self.E)
         ssd.ssd_matmul_i8(q, s, w["in_q"], w["in_s"], None, rows.view(T, self.E), self.status)
         _, xbc, dt_raw = self.slices(rows)
@@ -429,7 +430,7 @@ class SsdLayerDecoder:
                            l.params.decay_shift if l.params is not None else 7)
 
     def step(self, hidden, residual=None, stream=None):
-        """hidden [b, d] bf16, residual [b, d] fp32 or bf16, or None (the stream starts here, in fp32).  Returns
+        """hidden [b, d] bf16, residual [b, d] fp32 or bf16, or None (the stream starts here, in fp32), dense.  Returns
         (output [b, d] bf16, the residual to hand on).  stream: as in SsdLayer.prefill."""
         l, w = self.layer, self.layer.w
         if torch.cuda.current_device() != l.index:       # the scan's step launches on the current device

@@ -119,3 +119,15 @@ def test_residual_of_another_type_is_refused(torch_cuda):
         layer.prefill(hidden, res)
     with pytest.raises(iq.SsdError, match="residual"):
         layer.decoder(layer.zero_state(2)).step(hidden[:, 0].contiguous(), res[:, 0].contiguous())
+
+
+@pytest.mark.parametrize("path", ["bf16", "w8a8"])
+@pytest.mark.parametrize("lo", [1, 39])
+def test_prompts_that_are_slices_of_longer_ones(torch_cuda, path, lo):
+    """Up to a single token of a longer batch, its residual too, from a state: the bits of dense copies."""
+    torch = torch_cuda
+    layer = _layer(torch, path)
+    hidden, res = _hidden(torch, 2, 3, 40, D), _hidden(torch, 3, 3, 40, D).float()
+    state = layer.prefill(_hidden(torch, 4, 3, 9, D))[2]
+    ref = layer.prefill(hidden[:, lo:].contiguous(), res[:, lo:].contiguous(), state)
+    assert _same(layer.prefill(hidden[:, lo:], res[:, lo:], state), ref)

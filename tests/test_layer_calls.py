@@ -162,3 +162,15 @@ def test_a_residual_of_another_type_reaches_the_calls_own_check(world, monkeypat
     layer.prefill(torch.zeros(2, 1, D, dtype=torch.bfloat16), res[:, None])
     layer.decoder(layer.zero_state(2)).step(torch.zeros(2, D, dtype=torch.bfloat16), res)
     assert seen == [torch.float16] * 2
+
+
+@pytest.mark.parametrize("lo,hi", [(0, 5), (2, 4), (4, 5), (0, 1), (5, 5)])
+def test_prompts_that_are_slices_arrive_dense(world, monkeypatch, lo, hi):
+    layer, seen = make_layer("bf16"), []
+    layer.index = 0
+    monkeypatch.setattr(ssd, "ssd_add_rmsnorm_i8", lambda x, res, *a, **k: seen.extend((x, res)))
+    hidden = torch.randn(3, 5, 2 * D).bfloat16()[..., D:]
+    res = torch.randn(3, 5, D)
+    layer.prefill(hidden[:, lo:hi], res[:, lo:hi])
+    assert all(t.is_contiguous() for t in seen)
+    assert torch.equal(seen[0], hidden[:, lo:hi].reshape(-1, D)) and torch.equal(seen[1], res[:, lo:hi].reshape(-1, D))
