@@ -304,8 +304,9 @@ def _binding():
             from . import _binding as m
         except ImportError as e:
             raise ImportError(f"_binding.so is not built or does not load; run int8_quant_b200/build.py ({e})") from e
-        if m.torch_version != torch.__version__:
-            raise ImportError(f"_binding.so was built for torch {m.torch_version}, not {torch.__version__}; run "
+        built_for = getattr(m, "torch_version", "of an older build")
+        if built_for != torch.__version__:
+            raise ImportError(f"_binding.so was built for torch {built_for}, not {torch.__version__}; run "
                               "int8_quant_b200/build.py")
         _BINDING = m
     return _BINDING

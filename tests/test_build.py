@@ -76,3 +76,11 @@ def test_a_binding_for_another_torch_is_not_used(monkeypatch):
     monkeypatch.setattr(torch, "__version__", "0.0.1")
     with pytest.raises(ImportError, match="0.0.1"):
         ssd._binding()
+
+
+def test_a_binding_of_an_older_build_is_not_used(monkeypatch):
+    from int8_quant_b200 import ssd
+    monkeypatch.delattr(ssd._binding(), "torch_version")
+    monkeypatch.setattr(ssd, "_BINDING", None)
+    with pytest.raises(ImportError, match="older build"):
+        ssd._binding()
